@@ -70,6 +70,8 @@ extern "C" {
                                     [0, D] or a row id outside the pool: nothing written */
 #define SPECDEC_S_PROB 8         /* sampled verification met a position whose probabilities are all 0 */
 #define SPECDEC_S_ROWS_DUP 16    /* append: the same pool row listed twice (result undefined) */
+#define SPECDEC_S_TREE 32        /* a tree whose parents do not come before their children, or a path that is
+                                    none (see each call) */
 
 /* Library version string, e.g. "specdec 0.1 gfx950". */
 const char *specdec_version(void);
@@ -483,6 +485,169 @@ int specdec_paged_admit(const specdec_paged_t *kv, const int32_t *rows, int B, c
  * stack holds, set SPECDEC_S_LEN_RANGE; duplicate rows SPECDEC_S_ROWS_DUP
  * (nothing written either way).  Errors: E_ARG, E_LAUNCH. */
 int specdec_paged_retire(const specdec_paged_t *kv, const int32_t *rows, int B, int32_t *status, void *stream);
+
+/* ---------------------------------------------------------- trees of drafts */
+
+/* Speculation with a tree of drafts instead of a chain.  Row b's tree has N
+ * nodes (1 <= N <= SPECDEC_MAX_NODES), each a token the target scores in this
+ * round; node 0, the root, is the row's last committed token, which a chain
+ * scores at its first position.
+ *  parent  device int32 [B][N]: the parent of each node, 0 <= parent[b][i] < i
+ *          for i >= 1; -1 for a node that is not used (rows with smaller trees
+ *          are padded so); parent[b][0] is not read.  A node is part of the tree
+ *          if its parents lead to node 0.  Any other value sets SPECDEC_S_TREE
+ *          and counts as -1.
+ *  draft   device int32 [B][N]: each node's token id; draft[b][0] is not used.
+ * kv_new [layers][2][B][heads][N][head_dim] holds the nodes' KV entries, node
+ * 0's first.  A chain of D drafts is the tree of N = D + 1 nodes with parent
+ * {-, 0, 1, ...}; then draft[b][1 ..] are its drafts.
+ * One round: specdec_tree_positions, then per layer specdec_rope and
+ * specdec_tree_attention, then a verification, then specdec_tree_compact, whose
+ * outputs every append and realignment of this header takes as those of a chain
+ * of `depth` drafts. */
+#define SPECDEC_MAX_NODES 256
+
+/* Positions of the nodes: pos[b][i] (device int32 [B][N] out) = the row's
+ * content length + node i's depth, -1 for a node outside the tree.
+ *  len     device int32 [n_rows]: content lengths.
+ *  rows    device int32 [B], nullable: the row of each batch entry (NULL = b).
+ * Device conditions: rows outside [0, n_rows) or lengths outside [0, 2^30] set
+ * SPECDEC_S_LEN_RANGE (nothing written); SPECDEC_S_TREE.
+ * Limits: B <= 1024.  Errors: E_ARG, E_ALIAS, E_LAUNCH. */
+int specdec_tree_positions(const int32_t *parent, int B, int N, const int32_t *len, const int32_t *rows, int n_rows,
+                           int32_t *pos, int32_t *status, void *stream);
+
+/* Rotary positions.  The first `rot` elements of every head are rot/2 pairs;
+ * pair k of a token at position s turns by a = s * freq[k]:
+ *   y0 = factor * (x0 cos a - x1 sin a),  y1 = factor * (x1 cos a + x0 sin a).
+ * Pair k is elements (k, k + rot/2), or (2k, 2k+1) with `interleaved`.  Elements
+ * from rot on are copied.
+ *  x, out       device, element type `dtype`, [B][N][heads][head_dim]: strides
+ *               of row, node and head in elements (host int64[3]); a head is
+ *               contiguous.  out may be x with the same strides, or must not
+ *               overlap it (E_ALIAS, by the extents that the strides span).
+ *  pos          device int32 [B][N]; a token with a negative position is left as
+ *               it is in `out`.
+ *  freq         device fp64 [rot/2], radians per position; the angle is formed
+ *               and reduced in fp64, its sine and cosine are fp32.
+ * head_dim in [2, 1024] and rot in [2, head_dim], both even; heads <= 65535;
+ * B * N < 2^31.  An inverse rotation is one with the frequencies negated.
+ * Errors: E_ARG, E_DTYPE, E_ALIGN (a pointer not aligned to its elements),
+ * E_ALIAS, E_LAUNCH. */
+int specdec_rope(const void *x, const int64_t *x_strides, void *out, const int64_t *out_strides, int dtype, int B,
+                 int N, int heads, int head_dim, const int32_t *pos, const double *freq, int rot, int interleaved,
+                 float factor, void *stream);
+
+/* Attention of a tree's nodes over a cache: for node i of row b and query head h
+ * (of KV head h / (q_heads / heads)),
+ *   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q . k_j),
+ * over the row's cached positions and the nodes from i up to the root (itself
+ * included), whose keys and values are kv_new's.  A tree of one node is the
+ * attention of a single new token.
+ *  kv          the cache, of which layer `layer` is read: a left-padded rectangle
+ *              (kv->width not NULL: width[0], or with group > 0 width[b / group]
+ *              as a GATHER leaves them; rows must be NULL), a pool (kv->width
+ *              NULL), or pages.  Its pad, and positions past a row's length, are
+ *              not looked at.
+ *  rows        device int32 [B], nullable: the cache row of each batch entry
+ *              (NULL = b; a row may be listed more than once).
+ *  q, out      device, the cache's type, [B][N][q_heads][head_dim]: strides of
+ *              row, node and head in elements (host int64[3]), multiples of 16
+ *              bytes; a head is contiguous.  Nodes outside the tree are left as
+ *              they are in `out`.
+ *  kv_new      device [layers][2][B][heads][N][head_dim].
+ *  parent      the trees (above).  What nodes outside the tree hold in q and
+ *              kv_new has no effect, and what a node holds only reaches itself
+ *              and its descendants, whatever its values.
+ *  scale       finite, usually 1 / sqrt(head_dim).
+ *  ws          device workspace of specdec_tree_attention_workspace_bytes(B, N,
+ *              q_heads, heads, head_dim) bytes on the current device, 16-byte
+ *              aligned, cleared once by specdec_workspace_init; every call leaves
+ *              its counters cleared again.  Its size depends on N, q_heads / heads
+ *              and head_dim alone, so one workspace serves every layer and batch.
+ * Products are of the cache's type with fp32 sums; softmax sums are fp32 and the
+ * weights are rounded to the cache's type.
+ * Device conditions: lengths outside [0, cap] (or [0, width], [0, max_blocks *
+ * page]) or rows outside the cache set SPECDEC_S_LEN_RANGE (nothing written); a
+ * page id outside [0, n_pages) below a row's length sets it too, and that page's
+ * positions take no part; SPECDEC_S_TREE.
+ * Limits: B <= 1024, head_dim <= 256 and a multiple of 16 bytes, q_heads a
+ * multiple of heads and at most 1024 times as many, B * heads * N and the
+ * cache's rows * heads * cap (n_pages * heads * page) below 2^31.
+ * Errors: E_ARG, E_DTYPE, E_ALIGN, E_ALIAS, E_WORKSPACE, E_LAUNCH. */
+size_t specdec_tree_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, int head_dim);
+
+int specdec_tree_attention(const specdec_seqbuf_t *kv, const int32_t *rows, int group, int layer, const void *q,
+                           const int64_t *q_strides, int q_heads, const void *kv_new, const int32_t *parent, int B,
+                           int N, float scale, void *out, const int64_t *out_strides, void *ws, size_t ws_bytes,
+                           int32_t *status, void *stream);
+
+int specdec_tree_attention_paged(const specdec_paged_t *kv, const int32_t *rows, int layer, const void *q,
+                                 const int64_t *q_strides, int q_heads, const void *kv_new, const int32_t *parent,
+                                 int B, int N, float scale, void *out, const int64_t *out_strides, void *ws,
+                                 size_t ws_bytes, int32_t *status, void *stream);
+
+/* Greedy verification of a tree: from the root, the path goes to the child whose
+ * token is the target's choice at the node (the lowest such node where tokens
+ * repeat), until there is none or `depth` drafts are accepted.
+ *  logits      as for specdec_verify_greedy, rows (b, i) for i < N.
+ *  depth       accepted drafts at most, in [0, 255].
+ *  accept_len  device int32 [B] out: accepted drafts, in [0, depth].
+ *  next_token  device int32 [B] out: the target's choice at the last node.
+ *  path        device int32 [B][depth+1] out: the nodes from the root (0) to the
+ *              last one, then -1.
+ *  target_tok  device int32 [B][N] out, nullable: the choice at every node (of a
+ *              node outside the tree: at whatever its logits hold).
+ *  ws          as for specdec_verify_greedy with D = N - 1.
+ * SPECDEC_S_DRAFT_RANGE looks at nodes with a parent.  Errors: E_ARG (also
+ * B * N > 2^24, V > 2^30), E_DTYPE, E_WORKSPACE, E_ALIGN, E_LAUNCH. */
+int specdec_verify_tree_greedy(const void *logits, int dtype, int64_t row_stride, int B, int N, int V,
+                               const int32_t *draft, const int32_t *parent, int depth, int32_t *accept_len,
+                               int32_t *next_token, int32_t *path, int32_t *target_tok, void *ws, size_t ws_bytes,
+                               int32_t *status, void *stream);
+
+/* Sampled verification of a tree from the target's probabilities alone.  At a
+ * node with distribution p its children are tried in index order: with `left`
+ * the mass that is left (1 at first), child x is accepted iff
+ * u_accept[x's node] * left < p(x), else p(x) leaves `left` (all in fp64; a token
+ * that an earlier sibling holds too has no mass left).  Where none is accepted,
+ * or after `depth` accepted drafts, the next token is drawn from p, without the
+ * refused tokens of that node, by inverse CDF with u_draw[the node].  The tokens
+ * committed are distributed as the target's for any tree that was chosen
+ * without looking at the uniforms, so no draft probabilities are needed.  (For
+ * a chain drawn from a known q, specdec_verify_sample accepts more.)
+ *  p           device fp32 [B][N][V]: target probabilities at every node;
+ *              negative values and NaN count as 0.
+ *  u_accept, u_draw  device fp32 [B][N], uniforms in [0, 1).
+ *  next_token  the smallest id whose cumulative mass (fp64) exceeds u * total;
+ *              where the refused tokens held all of p's mass, p itself is drawn
+ *              from; an all-zero row gives id 0 and SPECDEC_S_PROB.
+ *  ws          as for specdec_verify_sample with D = N - 1.
+ * depth, accept_len, path and the other arguments as for
+ * specdec_verify_tree_greedy; a token outside [0, V) is refused
+ * (SPECDEC_S_DRAFT_RANGE).
+ * Errors: E_ARG (also B * N > 2^24, V > 2^30), E_WORKSPACE, E_ALIGN, E_LAUNCH. */
+int specdec_verify_tree_sample(const float *p, int B, int N, int V, const int32_t *draft, const int32_t *parent,
+                               const float *u_accept, const float *u_draw, int depth, int32_t *accept_len,
+                               int32_t *next_token, int32_t *path, void *ws, size_t ws_bytes, int32_t *status,
+                               void *stream);
+
+/* The accepted path's entries, in the form a chain's round leaves them: for j <=
+ * accept_len[b], kv_path[..][b][..][j] = kv_new[..][b][..][path[b][j]], and
+ * draft_path[b][j - 1] = draft[b][path[b][j]] for j >= 1.  Later entries are not
+ * written (nothing that takes kv_path and draft_path reads them).
+ *  kv_new      device [layers][2][B][heads][N][head_dim] of `dtype`.
+ *  kv_path     device [layers][2][B][heads][depth+1][head_dim] out.
+ *  draft_path  device int32 [B][depth] out.
+ * A row whose accepted length is outside [0, depth] or whose path leaves [0, N)
+ * sets SPECDEC_S_TREE, and nothing of that row is written.
+ * Limits: B <= 1024, head_dim * element size a multiple of 16 bytes, pointers
+ * 16-byte aligned (E_ALIGN); layers * 2 * heads * (depth+1) * head_dim * element
+ * size below 2^35 bytes.  Outputs must not overlap inputs (E_ALIAS).
+ * Errors: E_ARG, E_DTYPE, E_ALIGN, E_ALIAS, E_LAUNCH. */
+int specdec_tree_compact(const void *kv_new, int dtype, int layers, int B, int heads, int N, int head_dim,
+                         const int32_t *draft, const int32_t *path, const int32_t *accept_len, int depth,
+                         void *kv_path, int32_t *draft_path, int32_t *status, void *stream);
 
 #ifdef __cplusplus
 }

@@ -16,7 +16,9 @@ MEASURE_LIB = os.path.join(HERE, "libspecdec_measure.so")
 MEASURE_SOURCES = ["csrc/measure.hip"]
 OBJ = os.path.join(HERE, "_build")
 HIP_SOURCES = ["csrc/verify.hip", "csrc/realign.hip", "csrc/realign_inplace.hip", "csrc/sample_logits.hip",
-               "csrc/group.hip", "csrc/paged.hip", "csrc/pool.hip", "csrc/scratch.hip"]
+               "csrc/group.hip", "csrc/paged.hip", "csrc/pool.hip", "csrc/scratch.hip",
+               "csrc/tree.hip", "csrc/tree_sample.hip", "csrc/tree_attention_f32.hip", "csrc/tree_attention_f16.hip",
+               "csrc/tree_attention_bf16.hip"]
 CPP_SOURCES = ["csrc/api.cpp"]
 HIPCC = "/opt/rocm/bin/hipcc"
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I" + os.path.join(ROOT, "include")]

@@ -602,3 +602,359 @@ EXPORT int specdec_pool_admit(const specdec_seqbuf_t *pool, const specdec_sched_
   p.n_admitted = n_admitted;
   return launched(sd::launch_pool_admit(p, as_stream(stream)));
 }
+
+// ------------------------------------------------------------ trees of drafts
+
+static_assert(SPECDEC_MAX_NODES == sd::kMaxNodes, "the header states the node limit");
+
+static bool tree_shape_ok(int B, int N, int depth) {
+  return B >= 0 && N >= 1 && N <= sd::kMaxNodes && depth >= 0 && depth < sd::kMaxNodes && B <= (1 << 24) / N;
+}
+
+EXPORT int specdec_tree_positions(const int32_t *parent, int B, int N, const int32_t *len, const int32_t *rows,
+                                  int n_rows, int32_t *pos, int32_t *status, void *stream) {
+  if (!tree_shape_ok(B, N, 0) || B > sd::kMaxRealignRows || n_rows < 0) return SPECDEC_E_ARG;
+  if (B == 0) return SPECDEC_OK;
+  if (!parent || !len || !pos) return SPECDEC_E_ARG;
+  if (overlap(pos, (size_t)B * N * 4, parent, (size_t)B * N * 4) || overlap(pos, (size_t)B * N * 4, len, (size_t)n_rows * 4) ||
+      overlap(pos, (size_t)B * N * 4, rows, (size_t)B * 4))
+    return SPECDEC_E_ALIAS;
+  sd::TreePosParams p;
+  p.parent = parent;
+  p.len = len;
+  p.rows = rows;
+  p.B = B;
+  p.N = N;
+  p.n_rows = n_rows;
+  p.pos = pos;
+  p.status = status;
+  return launched(sd::launch_tree_positions(p, as_stream(stream)));
+}
+
+// First and last byte offsets that a [B][N][H][Dh] tensor of the given strides
+// touches, or false where they pass 62 bits.
+static bool extent(const int64_t *st, int B, int N, int H, int Dh, size_t es, int64_t &lo, int64_t &hi) {
+  const int n[3] = {B, N, H};
+  __int128 a = 0, z = Dh - 1;
+  for (int k = 0; k < 3; ++k) {
+    const __int128 d = (__int128)st[k] * (n[k] - 1);
+    (d < 0 ? a : z) += d;
+  }
+  a *= (int)es;
+  z = (z + 1) * (int)es;
+  if (a < -((__int128)1 << 62) || z > ((__int128)1 << 62)) return false;
+  lo = (int64_t)a;
+  hi = (int64_t)z;
+  return true;
+}
+
+EXPORT int specdec_rope(const void *x, const int64_t *x_strides, void *out, const int64_t *out_strides, int dtype,
+                        int B, int N, int heads, int head_dim, const int32_t *pos, const double *freq, int rot,
+                        int interleaved, float factor, void *stream) {
+  if (B < 0 || N < 0 || heads < 1 || heads > 65535 || head_dim < 2 || head_dim > 1024 || head_dim % 2)
+    return SPECDEC_E_ARG;
+  if (rot < 2 || rot > head_dim || rot % 2 || !isfinite(factor)) return SPECDEC_E_ARG;
+  if (!dtype_ok(dtype)) return SPECDEC_E_DTYPE;
+  if (B == 0 || N == 0) return SPECDEC_OK;
+  if ((long long)B * N >= (1LL << 31)) return SPECDEC_E_ARG;
+  if (!x || !out || !x_strides || !out_strides || !pos || !freq) return SPECDEC_E_ARG;
+  const size_t es = esize(dtype);
+  if (reinterpret_cast<uintptr_t>(x) % es || reinterpret_cast<uintptr_t>(out) % es) return SPECDEC_E_ALIGN;
+  int64_t xl, xh, ol, oh;
+  if (!extent(x_strides, B, N, heads, head_dim, es, xl, xh) || !extent(out_strides, B, N, heads, head_dim, es, ol, oh))
+    return SPECDEC_E_ARG;
+  const char *xp = static_cast<const char *>(x);
+  char *op = static_cast<char *>(out);
+  bool same = x == out;  // in place: the same values, each read and written by one thread
+  const int n[3] = {B, N, heads};
+  for (int k = 0; k < 3; ++k) same = same && (n[k] == 1 || x_strides[k] == out_strides[k]);
+  if (!same && overlap(xp + xl, (size_t)(xh - xl), op + ol, (size_t)(oh - ol))) return SPECDEC_E_ALIAS;
+  sd::RopeParams p;
+  memset(&p, 0, sizeof(p));
+  p.x = x;
+  p.out = out;
+  p.dtype = dtype;
+  p.B = B;
+  p.N = N;
+  p.heads = heads;
+  p.Dh = head_dim;
+  p.rot = rot;
+  p.pos = pos;
+  p.freq = freq;
+  p.factor = factor;
+  p.interleaved = interleaved != 0;
+  // a dimension of one entry has no stride that matters
+  uint64_t mix = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out);
+  for (int k = 0; k < 3; ++k) {
+    p.xs[k] = n[k] > 1 ? x_strides[k] : 0;
+    p.os[k] = n[k] > 1 ? out_strides[k] : 0;
+    mix |= (uint64_t)p.xs[k] * es | (uint64_t)p.os[k] * es;
+  }
+  p.ve = (int)(16 / es);
+  while (p.ve > 1 && mix % ((uint64_t)p.ve * es)) p.ve /= 2;
+  return launched(sd::launch_rope(p, as_stream(stream)));
+}
+
+EXPORT int specdec_verify_tree_greedy(const void *logits, int dtype, int64_t row_stride, int B, int N, int V,
+                                      const int32_t *draft, const int32_t *parent, int depth, int32_t *accept_len,
+                                      int32_t *next_token, int32_t *path, int32_t *target_tok, void *ws,
+                                      size_t ws_bytes, int32_t *status, void *stream) {
+  if (!tree_shape_ok(B, N, depth) || V < 1 || V > (1 << 30) || row_stride < V) return SPECDEC_E_ARG;
+  if (!dtype_ok(dtype)) return SPECDEC_E_DTYPE;
+  if (B == 0) return SPECDEC_OK;
+  if (!logits || !draft || !parent || !accept_len || !next_token || !path) return SPECDEC_E_ARG;
+  if (!ws || ws_bytes < specdec_workspace_bytes(B, N - 1) || reinterpret_cast<uintptr_t>(ws) % 8 != 0)
+    return SPECDEC_E_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(logits) % esize(dtype)) return SPECDEC_E_ALIGN;
+  sd::GreedyParams p;
+  p.logits = logits;
+  p.dtype = dtype;
+  p.row_stride = row_stride;
+  p.B = B;
+  p.D = N - 1;
+  p.V = V;
+  p.draft = draft;
+  p.accept_len = accept_len;
+  p.next_token = next_token;
+  p.target_tok = target_tok;
+  p.keys = static_cast<unsigned long long *>(ws);
+  p.counters = reinterpret_cast<unsigned int *>(static_cast<char *>(ws) + ws_keys_bytes(B, N - 1));
+  p.status = status;
+  p.vec = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && ((size_t)row_stride * esize(dtype)) % 16 == 0;
+  p.parent = parent;
+  p.path = path;
+  p.depth = depth;
+  return launched(sd::launch_verify_tree_greedy(p, as_stream(stream)));
+}
+
+EXPORT int specdec_verify_tree_sample(const float *p, int B, int N, int V, const int32_t *draft,
+                                      const int32_t *parent, const float *u_accept, const float *u_draw, int depth,
+                                      int32_t *accept_len, int32_t *next_token, int32_t *path, void *ws,
+                                      size_t ws_bytes, int32_t *status, void *stream) {
+  if (!tree_shape_ok(B, N, depth) || V < 1 || V > (1 << 30)) return SPECDEC_E_ARG;
+  if (B == 0) return SPECDEC_OK;
+  if (!p || !draft || !parent || !u_accept || !u_draw || !accept_len || !next_token || !path) return SPECDEC_E_ARG;
+  if (!ws || ws_bytes < specdec_verify_sample_workspace_bytes(B, N - 1, V) || reinterpret_cast<uintptr_t>(ws) % 16 != 0)
+    return SPECDEC_E_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(p) % 4) return SPECDEC_E_ALIGN;
+  sd::TreeSampleParams s;
+  s.p = p;
+  s.B = B;
+  s.N = N;
+  s.V = V;
+  s.depth = depth;
+  sd::sample_shape(V, s.R, s.S);
+  s.draft = draft;
+  s.parent = parent;
+  s.u_accept = u_accept;
+  s.u_draw = u_draw;
+  s.accept_len = accept_len;
+  s.next_token = next_token;
+  s.path = path;
+  s.status = status;
+  s.ws = static_cast<char *>(ws);
+  return launched(sd::launch_verify_tree_sample(s, as_stream(stream)));
+}
+
+EXPORT int specdec_tree_compact(const void *kv_new, int dtype, int layers, int B, int heads, int N, int head_dim,
+                                const int32_t *draft, const int32_t *path, const int32_t *accept_len, int depth,
+                                void *kv_path, int32_t *draft_path, int32_t *status, void *stream) {
+  if (!tree_shape_ok(B, N, depth) || B > sd::kMaxRealignRows || layers < 0 || heads < 1 || head_dim < 1)
+    return SPECDEC_E_ARG;
+  if (!dtype_ok(dtype)) return SPECDEC_E_DTYPE;
+  if (B == 0) return SPECDEC_OK;
+  const size_t pos_bytes = (size_t)head_dim * esize(dtype);
+  if (pos_bytes % 16 != 0) return SPECDEC_E_ALIGN;
+  if (!draft || !path || !accept_len || (depth > 0 && !draft_path)) return SPECDEC_E_ARG;
+  if (layers > 0 && (!kv_new || !kv_path)) return SPECDEC_E_ARG;
+  if (reinterpret_cast<uintptr_t>(kv_new) % 16 != 0 || reinterpret_cast<uintptr_t>(kv_path) % 16 != 0)
+    return SPECDEC_E_ALIGN;
+  // a row's units are numbered with 32-bit integers
+  const __int128 seqs = (__int128)layers * 2 * heads;
+  const __int128 row_units = seqs * (depth + 1) * (__int128)(pos_bytes / 16);
+  if (seqs >= (1LL << 30) || pos_bytes / 16 > (1u << 20) || row_units >= (1LL << 31)) return SPECDEC_E_ARG;
+  const size_t in_bytes = (size_t)seqs * B * N * pos_bytes, out_bytes = (size_t)seqs * B * (depth + 1) * pos_bytes;
+  const size_t rows4 = (size_t)B * 4;
+  const void *ins[4] = {kv_new, draft, path, accept_len};
+  const size_t in_n[4] = {in_bytes, rows4 * N, rows4 * (depth + 1), rows4};
+  for (int k = 0; k < 4; ++k)
+    if (overlap(ins[k], in_n[k], kv_path, out_bytes) || overlap(ins[k], in_n[k], draft_path, rows4 * depth))
+      return SPECDEC_E_ALIAS;
+  sd::CompactParams p;
+  memset(&p, 0, sizeof(p));
+  p.kv_new = kv_new;
+  p.kv_path = kv_path;
+  p.seqs = (int)seqs;
+  p.B = B;
+  p.H = heads;
+  p.N = N;
+  p.depth = depth;
+  p.units = (int)(pos_bytes / 16);
+  p.draft = draft;
+  p.path = path;
+  p.accept_len = accept_len;
+  p.draft_path = draft_path;
+  p.status = status;
+  return launched(sd::launch_tree_compact(p, as_stream(stream)));
+}
+
+// Query tiles by the number of query rows M = N * Hq / Hkv of a KV head: few
+// rows leave all four waves to the keys; more rows go to more tiles per wave,
+// then to more waves.
+namespace sd {
+AttnShape attn_shape(int dtype, int Dh, int M) {
+  AttnShape a;
+  a.dhp = Dh <= 64 ? 64 : Dh <= 128 ? 128 : 256;
+  const int most = attn_most_tiles(dtype, a.dhp), tiles = (M + 15) / 16;
+  if (tiles <= most) {
+    a.rw = 1;
+    a.rt = tiles == 3 ? 4 : tiles;
+  } else {
+    a.rw = tiles <= 2 * most ? 2 : 4;
+    a.rt = a.rw == 2 && most >= 4 && tiles <= 6 ? 3 : most;
+  }
+  return a;
+}
+
+// Workgroups of a launch: what fits the CUs at once.
+int attn_grid(const AttnShape &a) {
+  return (device_cus() * attn_wgs_per_cu(a.rt, a.dhp) + 7) / 8 * 8;
+}
+}  // namespace sd
+
+EXPORT size_t specdec_tree_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, int head_dim) {
+  if (!tree_shape_ok(B, N, 0) || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads || head_dim < 1 ||
+      head_dim > 256 || q_heads / kv_heads > 1024)
+    return 0;
+  size_t most = 0;
+  for (int dt = 0; dt < 3; ++dt) {
+    const sd::AttnShape a = sd::attn_shape(dt, head_dim, N * (q_heads / kv_heads));
+    const size_t n = (size_t)sd::attn_grid(a) * (sd::kAtomicLine + a.wg_bytes());
+    most = n > most ? n : most;
+  }
+  return most;
+}
+
+static bool strides_ok(const int64_t *st, int B, int N, int H, int Dh, size_t es, int64_t &lo, int64_t &hi, bool &aligned) {
+  const int n[3] = {B, N, H};
+  for (int k = 0; k < 3; ++k)
+    if (n[k] > 1 && (uint64_t)st[k] * es % 16 != 0) aligned = false;
+  return extent(st, B, N, H, Dh, es, lo, hi);
+}
+
+// What both cache forms share; `old_bytes` the cache's extent.
+static int attention(sd::TreeAttnParams &p, const void *kv, size_t old_bytes, int dtype, const void *q,
+                     const int64_t *q_strides, int q_heads, const void *kv_new, int layers, int layer,
+                     float scale, void *out, const int64_t *out_strides, void *ws, size_t ws_bytes, void *stream) {
+  const int B = p.B, N = p.N, H = p.H, Dh = p.Dh;
+  const size_t es = esize(dtype);
+  if (Dh > 256 || q_heads < H || q_heads % H || q_heads / H > 1024 || q_heads > 65535) return SPECDEC_E_ARG;
+  if (layer < 0 || layer >= layers || !isfinite(scale)) return SPECDEC_E_ARG;
+  if (B == 0) return SPECDEC_OK;
+  if (!q || !q_strides || !out || !out_strides || !kv_new || !p.parent) return SPECDEC_E_ARG;
+  p.G = q_heads / H;
+  int64_t ql, qh, ol, oh;
+  bool aligned = reinterpret_cast<uintptr_t>(q) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
+                 reinterpret_cast<uintptr_t>(kv_new) % 16 == 0;
+  if (!strides_ok(q_strides, B, N, q_heads, Dh, es, ql, qh, aligned) ||
+      !strides_ok(out_strides, B, N, q_heads, Dh, es, ol, oh, aligned))
+    return SPECDEC_E_ARG;
+  if (!aligned) return SPECDEC_E_ALIGN;
+  const size_t half = (size_t)B * H * N * Dh * es;
+  // rows of a head (KV positions) are numbered with 32-bit integers
+  if ((__int128)B * H * N >= (1LL << 31)) return SPECDEC_E_ARG;
+  const char *nk = static_cast<const char *>(kv_new) + (size_t)layer * 2 * half;
+  char *op = static_cast<char *>(out) + ol;
+  const size_t on = (size_t)(oh - ol), four = (size_t)B * 4;
+  if (overlap(op, on, static_cast<const char *>(q) + ql, (size_t)(qh - ql)) || overlap(op, on, nk, 2 * half) ||
+      overlap(op, on, kv, old_bytes) || overlap(op, on, p.parent, four * N) || overlap(op, on, p.rows, four) ||
+      overlap(op, on, p.len, (size_t)p.n_rows * 4) || overlap(op, on, ws, ws_bytes))
+    return SPECDEC_E_ALIAS;
+  const sd::AttnShape a = sd::attn_shape(dtype, Dh, N * p.G);
+  p.grid = sd::attn_grid(a);
+  const size_t counters = (size_t)p.grid * sd::kAtomicLine, partial = (size_t)p.grid * a.wg_bytes();
+  if (!ws || ws_bytes < counters + partial || reinterpret_cast<uintptr_t>(ws) % 16 != 0) return SPECDEC_E_WORKSPACE;
+  if (partial >= (1u << 31)) return SPECDEC_E_ARG;
+  p.q = q;
+  p.out = out;
+  for (int k = 0; k < 3; ++k) {
+    p.qs[k] = q_strides[k];
+    p.os[k] = out_strides[k];
+  }
+  p.k_new = nk;
+  p.v_new = nk + half;
+  p.scale = (float)((double)scale * 1.44269504088896340736);  // log2(e): the kernel's exponentials are of base 2
+  p.counters = static_cast<unsigned int *>(ws);
+  p.partial = static_cast<char *>(ws) + counters;
+  p.partial_bytes = (int)partial;
+  p.page_div = sd::host_fast_div((uint32_t)(p.page > 0 ? p.page : 1));
+  p.g_div = sd::host_fast_div((uint32_t)p.G);
+  hipStream_t s = as_stream(stream);
+  return launched(dtype == SPECDEC_F32   ? sd::launch_tree_attention_f32(p, s)
+                  : dtype == SPECDEC_F16 ? sd::launch_tree_attention_f16(p, s)
+                                         : sd::launch_tree_attention_bf16(p, s));
+}
+
+EXPORT int specdec_tree_attention(const specdec_seqbuf_t *kv, const int32_t *rows, int group, int layer, const void *q,
+                                  const int64_t *q_strides, int q_heads, const void *kv_new, const int32_t *parent,
+                                  int B, int N, float scale, void *out, const int64_t *out_strides, void *ws,
+                                  size_t ws_bytes, int32_t *status, void *stream) {
+  const int rc = check_seqbuf_shape(kv);
+  if (rc) return rc;
+  if (!tree_shape_ok(B, N, 0) || B > sd::kMaxAttnRows || group < 0) return SPECDEC_E_ARG;
+  if ((!rows && B > kv->rows) || (rows && kv->width)) return SPECDEC_E_ARG;  // a rectangle's rows are its batch
+  if ((__int128)kv->rows * kv->heads * kv->cap >= (1LL << 31)) return SPECDEC_E_ARG;
+  sd::TreeAttnParams p;
+  memset(&p, 0, sizeof(p));
+  const size_t half = kv_bytes(kv) / (2 * (size_t)(kv->layers > 0 ? kv->layers : 1));
+  const char *base = static_cast<const char *>(kv->kv) + (layer > 0 ? (size_t)layer * 2 * half : 0);
+  p.k_old = base;
+  p.v_old = base + half;
+  p.len = kv->len;
+  p.rows = rows;
+  p.width = kv->width;
+  p.n_rows = kv->rows;
+  p.cap = kv->cap;
+  p.group = group;
+  p.parent = parent;
+  p.B = B;
+  p.N = N;
+  p.H = kv->heads;
+  p.Dh = kv->head_dim;
+  p.status = status;
+  return attention(p, kv->kv, kv_bytes(kv), kv->dtype, q, q_strides, q_heads, kv_new, kv->layers, layer, scale, out,
+                   out_strides, ws, ws_bytes, stream);
+}
+
+EXPORT int specdec_tree_attention_paged(const specdec_paged_t *kv, const int32_t *rows, int layer, const void *q,
+                                        const int64_t *q_strides, int q_heads, const void *kv_new,
+                                        const int32_t *parent, int B, int N, float scale, void *out,
+                                        const int64_t *out_strides, void *ws, size_t ws_bytes, int32_t *status,
+                                        void *stream) {
+  const int rc = check_paged(kv);
+  if (rc) return rc;
+  if (!tree_shape_ok(B, N, 0) || B > sd::kMaxAttnRows || (!rows && B > kv->rows)) return SPECDEC_E_ARG;
+  if ((__int128)kv->n_pages * kv->heads * kv->page >= (1LL << 31)) return SPECDEC_E_ARG;
+  sd::TreeAttnParams p;
+  memset(&p, 0, sizeof(p));
+  const size_t half = paged_bytes(kv) / (2 * (size_t)(kv->layers > 0 ? kv->layers : 1));
+  const char *base = static_cast<const char *>(kv->pages) + (layer > 0 ? (size_t)layer * 2 * half : 0);
+  p.k_old = base;
+  p.v_old = base + half;
+  p.table = kv->block_table;
+  p.max_blocks = kv->max_blocks;
+  p.page = kv->page;
+  p.n_pages = kv->n_pages;
+  p.len = kv->len;
+  p.rows = rows;
+  p.n_rows = kv->rows;
+  p.cap = kv->max_blocks * kv->page;
+  p.parent = parent;
+  p.B = B;
+  p.N = N;
+  p.H = kv->heads;
+  p.Dh = kv->head_dim;
+  p.status = status;
+  return attention(p, kv->pages, paged_bytes(kv), kv->dtype, q, q_strides, q_heads, kv_new, kv->layers, layer, scale,
+                   out, out_strides, ws, ws_bytes, stream);
+}

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "device_common.h"
 #include "realign_params.h"
 
 namespace sd {
@@ -20,6 +21,10 @@ struct GreedyParams {
   unsigned int *counters;
   int32_t *status;
   bool vec;                   // 16-byte aligned rows: vector loads
+  // trees (launch_verify_tree_greedy): D + 1 nodes per row
+  const int32_t *parent;      // [B][D+1]
+  int32_t *path;              // [B][depth+1]
+  int depth;                  // nodes below the root that a row accepts at most
 };
 
 // Words that many workgroups update with device-scope atomics each get a
@@ -29,6 +34,82 @@ struct GreedyParams {
 constexpr int kAtomicLine = 128;
 constexpr int kKeyStride = kAtomicLine / 8;
 constexpr int kCountStride = kAtomicLine / 4;
+
+// Trees of drafted tokens (see tree_common.h).
+constexpr int kMaxNodes = 256;           // nodes of a tree
+constexpr int kMaxTreeLen = 1 << 30;     // content positions a tree's root may stand at
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 16;          // tokens one rotary workgroup turns at most
+
+// Tree attention.
+constexpr int kMaxAttnRows = 1024;       // batch rows (their lengths' prefix sums are kept in LDS)
+
+// Query rows of a workgroup: rw waves of rt 16-row tiles, the other 4 / rw waves
+// taking other keys; the head size is padded to dhp.
+struct AttnShape {
+  int dhp, rt, rw;
+  int rows() const { return rw * rt * 16; }
+  // partial results of one workgroup (two segments at most): per query row O, then max and sum
+  size_t wg_bytes() const { return (size_t)2 * rows() * (dhp + 4) * 4; }
+};
+
+// 16-row query tiles a wave can hold beside its keys in 512 registers.
+constexpr int attn_most_tiles(int dtype, int dhp) {
+  return dtype == 0 ? (dhp == 256 ? 1 : 2) : (dhp == 256 ? 2 : 4);
+}
+// Workgroups per CU that the registers and LDS of an instance are held to.
+constexpr int attn_wgs_per_cu(int rt, int dhp) { return rt <= 2 && dhp <= 128 ? 2 : 1; }
+AttnShape attn_shape(int dtype, int Dh, int M);
+int attn_grid(const AttnShape &a);
+
+struct TreeAttnParams {
+  const void *q;                         // strided (row, node, query head), Dh contiguous
+  void *out;
+  int64_t qs[3], os[3];                  // in elements
+  const void *k_old, *v_old;             // this layer's K and V: rows of Dh elements
+  const void *k_new, *v_new;             // [B][H][N][Dh]
+  const int32_t *table;                  // paged: [n_rows][max_blocks], else NULL
+  int max_blocks, page, n_pages;
+  const int32_t *len, *rows, *width;     // [n_rows]; [B] or NULL; rectangle widths or NULL
+  int n_rows, cap, group;
+  const int32_t *parent;                 // [B][N]
+  int B, N, H, G, Dh;
+  float scale;                           // times log2(e)
+  unsigned int *counters;                // workspace: a line per workgroup, zero between calls
+  void *partial;
+  int partial_bytes, grid;
+  int32_t *status;
+  FastDiv page_div, g_div;
+};
+
+struct TreePosParams {
+  const int32_t *parent, *len, *rows;    // [B][N], [n_rows], [B] (nullable = identity)
+  int B, N, n_rows;
+  int32_t *pos, *status;                 // [B][N]
+};
+
+struct RopeParams {
+  const void *x;
+  void *out;
+  int64_t xs[3], os[3];                  // strides of row, node, head in elements
+  int dtype, B, N, heads, Dh, rot;
+  const int32_t *pos;                    // [B][N]
+  const double *freq;                    // [rot / 2] radians per position
+  float factor;
+  bool interleaved;
+  int ve;                                // elements per access that pointers and strides allow (1 to 16 bytes)
+  int tokens;                            // per workgroup (set by the launcher, with the divisors)
+  FastDiv half_div, head_div, token_div, node_div;
+};
+
+struct CompactParams {
+  const void *kv_new;                    // [seqs / H][B][H][N][units * 16 bytes]
+  void *kv_path;                         // [seqs / H][B][H][depth + 1][units * 16 bytes]
+  int seqs, B, H, N, depth, units;       // seqs = layers * 2 * heads
+  const int32_t *draft, *path, *accept_len;  // [B][N], [B][depth + 1], [B]
+  int32_t *draft_path, *status;          // [B][depth]
+  FastDiv unit_div, head_div;
+};
 
 struct SampleParams {
   const float *p, *q;
@@ -48,6 +129,16 @@ constexpr int kSampleThreads = 256;  // threads per sampled-verification workgro
 constexpr int kSampleSplits = 16;    // workgroups per batch row at most (runs grow with V beyond 32768)
 constexpr size_t kSampleRowBytes = kAtomicLine + (size_t)kSampleSplits * 16 + (size_t)kSampleSplits * kSampleThreads * 16;
 void sample_shape(int V, int &R, int &S);
+
+struct TreeSampleParams {
+  const float *p;             // [B][N][V]
+  int B, N, V, depth;
+  int R, S;                   // as for sampled verification of a chain, the workspace too
+  const int32_t *draft, *parent;         // [B][N]
+  const float *u_accept, *u_draw;        // [B][N]
+  int32_t *accept_len, *next_token, *path, *status;
+  char *ws;
+};
 
 struct SampleLogitsParams {
   const void *target, *draftl;  // logits [B][D+1][V] and [B][D][V] of `dtype`
@@ -162,12 +253,20 @@ struct PoolParams {
 };
 
 hipError_t launch_verify_greedy(const GreedyParams &p, hipStream_t s);
+hipError_t launch_verify_tree_greedy(const GreedyParams &p, hipStream_t s);
 hipError_t launch_verify_sample(const SampleParams &p, hipStream_t s);
+hipError_t launch_verify_tree_sample(const TreeSampleParams &p, hipStream_t s);
 hipError_t launch_verify_sample_logits(const SampleLogitsParams &p, hipStream_t s);
 hipError_t launch_group_by_len(const GroupParams &p, hipStream_t s);
 hipError_t launch_paged(const PagedParams &p, hipStream_t s);
 hipError_t launch_pool_finish(const PoolParams &p, hipStream_t s);
 hipError_t launch_pool_admit(const PoolParams &p, hipStream_t s);
+hipError_t launch_tree_positions(const TreePosParams &p, hipStream_t s);
+hipError_t launch_tree_attention_f32(const TreeAttnParams &p, hipStream_t s);
+hipError_t launch_tree_attention_f16(const TreeAttnParams &p, hipStream_t s);
+hipError_t launch_tree_attention_bf16(const TreeAttnParams &p, hipStream_t s);
+hipError_t launch_rope(const RopeParams &p, hipStream_t s);
+hipError_t launch_tree_compact(CompactParams p, hipStream_t s);
 hipError_t launch_zero(void *ptr, size_t bytes, hipStream_t s);
 hipError_t static_scratch(void **out, hipStream_t s);
 

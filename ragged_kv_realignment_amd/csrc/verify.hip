@@ -10,11 +10,16 @@
 // verification follows section "Exactness Means Different Things For Greedy
 // And Sampled Output": accept with probability min(1, p/q), replace from
 // normalize(max(0, p - q)), take the bonus from p after the full draft.
+//
+// A tree of drafts takes the same greedy kernel with another finish: the
+// target's choice is found at every node, then the path of nodes that continue
+// it is followed from the root.
 #include <math.h>
 #include <limits.h>
 #include "coherent.h"
 #include "device_common.h"
 #include "launch.h"
+#include "tree_common.h"
 #include "wave_dpp.h"
 #include "specdec.h"
 
@@ -126,7 +131,13 @@ __device__ __forceinline__ float wave_max_uniform(float v) {
 // and the last workgroup's key loads observe all of them.  A compiler that
 // moved the count ahead of the max would break property 2; the dependency
 // through the inline asm is what forbids it.
-template <int DT, bool VEC, int NT, int VPT>
+//
+// TREE: the D + 1 rows of a batch row are the nodes of a tree, draft holds a
+// token for each of them and parent its place.  The finish marks every node
+// whose token is its parent's choice in the parent's LDS slot (the lowest such
+// node stays), in parallel; thread 0 then follows the slots from the root, one
+// LDS round trip per accepted token.
+template <int DT, bool VEC, int NT, int VPT, bool TREE>
 __global__ __launch_bounds__(NT) void k_verify_greedy(GreedyParams p, int splits, int chunk, FastDiv rows_div,
                                                       FastDiv d1_div) {
   constexpr int ES = Elem<DT>::size;
@@ -224,6 +235,44 @@ __global__ __launch_bounds__(NT) void k_verify_greedy(GreedyParams p, int splits
   // cleared only after the outputs, so no wait covers those stores.
   const int i = threadIdx.x;
   unsigned long long *kp = &p.keys[((size_t)b * D1 + min(i, D)) * kKeyStride];
+  if constexpr (TREE) {
+    __shared__ int s_next[NT];  // the lowest accepted child of each node, D1 = none
+    int tok = 0, par = -1;
+    if (i < D1) {
+      bool bad = false;
+      tok = p.draft[(size_t)b * D1 + i];
+      par = i > 0 ? node_parent(i, p.parent[(size_t)b * D1 + i], bad) : -1;
+      const int t = key_id(load_agent(kp));
+      s_t[i] = t;
+      s_next[i] = D1;
+      if (p.target_tok) p.target_tok[(size_t)b * D1 + i] = t;
+      const int flags = (bad ? SPECDEC_S_TREE : 0) | (par >= 0 && (tok < 0 || tok >= p.V) ? SPECDEC_S_DRAFT_RANGE : 0);
+      if (flags) atomicOr(&s_bad, flags);
+    }
+    __syncthreads();
+    if (par >= 0 && tok >= 0 && tok == s_t[par]) atomicMin(&s_next[par], i);
+    __syncthreads();
+    if (i == 0) {
+      int32_t *path = p.path + (size_t)b * (p.depth + 1);
+      int cur = 0, a = 0;
+      path[0] = 0;
+      while (a < p.depth) {
+        const int c = s_next[cur];
+        if (c >= D1) break;
+        cur = c;
+        path[++a] = cur;
+      }
+      s_a = a;
+      p.accept_len[b] = a;
+      p.next_token[b] = s_t[cur];
+      store_agent(&p.counters[(size_t)b * kCountStride], 0u);
+      set_status(p.status, s_bad);
+    }
+    __syncthreads();
+    if (i > s_a && i <= p.depth) p.path[(size_t)b * (p.depth + 1) + i] = -1;
+    if (i < D1) store_agent(kp, 0ull);
+    return;
+  }
   if (i < D1) {
     const int d = i < D ? p.draft[(size_t)b * D + i] : 0;
     const int t = key_id(load_agent(kp));
@@ -265,7 +314,7 @@ static long greedy_chunk(int B, int D, int V, int dtype) {
   return chunk;
 }
 
-template <int DT>
+template <int DT, bool TREE>
 static hipError_t launch_greedy_dt(const GreedyParams &p, hipStream_t s) {
   const long rows = (long)p.B * (p.D + 1);
   const long chunk = greedy_chunk(p.B, p.D, p.V, DT);
@@ -273,18 +322,24 @@ static hipError_t launch_greedy_dt(const GreedyParams &p, hipStream_t s) {
   const dim3 grid((unsigned)(rows * splits));
   const FastDiv rows_div = host_fast_div((uint32_t)rows), d1_div = host_fast_div((uint32_t)(p.D + 1));
   if (p.vec)
-    hipLaunchKernelGGL((k_verify_greedy<DT, true, kBlock, SPECDEC_VG_VPT>), grid, dim3(kBlock), 0, s, p, splits,
+    hipLaunchKernelGGL((k_verify_greedy<DT, true, kBlock, SPECDEC_VG_VPT, TREE>), grid, dim3(kBlock), 0, s, p, splits,
                        (int)chunk, rows_div, d1_div);
   else
-    hipLaunchKernelGGL((k_verify_greedy<DT, false, kBlock, SPECDEC_VG_VPT>), grid, dim3(kBlock), 0, s, p, splits,
+    hipLaunchKernelGGL((k_verify_greedy<DT, false, kBlock, SPECDEC_VG_VPT, TREE>), grid, dim3(kBlock), 0, s, p, splits,
                        (int)chunk, rows_div, d1_div);
   return hipGetLastError();
 }
 
 hipError_t launch_verify_greedy(const GreedyParams &p, hipStream_t s) {
-  if (p.dtype == 0) return launch_greedy_dt<0>(p, s);
-  if (p.dtype == 1) return launch_greedy_dt<1>(p, s);
-  return launch_greedy_dt<2>(p, s);
+  if (p.dtype == 0) return launch_greedy_dt<0, false>(p, s);
+  if (p.dtype == 1) return launch_greedy_dt<1, false>(p, s);
+  return launch_greedy_dt<2, false>(p, s);
+}
+
+hipError_t launch_verify_tree_greedy(const GreedyParams &p, hipStream_t s) {
+  if (p.dtype == 0) return launch_greedy_dt<0, true>(p, s);
+  if (p.dtype == 1) return launch_greedy_dt<1, true>(p, s);
+  return launch_greedy_dt<2, true>(p, s);
 }
 
 // ---------------------------------------------------------------- sampled

@@ -6,6 +6,7 @@ and every step runs in the library's HIP kernels.  There is no fallback: if the
 library is missing, calls raise.
 """
 import ctypes as C
+import math
 import os
 
 import torch
@@ -16,7 +17,7 @@ LIB_PATH = os.path.join(HERE, "libspecdec.so")
 F32, F16, BF16 = 0, 1, 2
 EQSPEC, GATHER, APPEND_INPLACE, EQSPEC_INPLACE, EQSPEC_INPLACE_ZERO_PAD = 0, 1, 2, 3, 4
 OK, E_ARG, E_DTYPE, E_WORKSPACE, E_ALIAS, E_ALIGN, E_LAUNCH, E_SCRATCH = 0, -1, -2, -3, -4, -5, -6, -7
-S_DRAFT_RANGE, S_CAPACITY, S_LEN_RANGE, S_PROB, S_ROWS_DUP = 1, 2, 4, 8, 16
+S_DRAFT_RANGE, S_CAPACITY, S_LEN_RANGE, S_PROB, S_ROWS_DUP, S_TREE = 1, 2, 4, 8, 16, 32
 
 _ERRORS = {E_ARG: "invalid argument", E_DTYPE: "unsupported element type", E_WORKSPACE: "workspace too small",
            E_ALIAS: "output overlaps an input", E_ALIGN: "misaligned KV buffer", E_LAUNCH: "kernel launch failed",
@@ -27,7 +28,10 @@ EXPORTS = ("specdec_version", "specdec_workspace_bytes", "specdec_workspace_init
            "specdec_verify_sample", "specdec_sample_workspace_bytes", "specdec_verify_sample_logits",
            "specdec_realign_kv", "specdec_group_by_len", "specdec_paged_append", "specdec_paged_gather",
            "specdec_paged_admit", "specdec_paged_retire", "specdec_group_by_len_ids", "specdec_pool_finish",
-           "specdec_pool_admit", "specdec_verify_greedy_noalloc", "specdec_verify_sample_workspace_bytes")
+           "specdec_pool_admit", "specdec_verify_greedy_noalloc", "specdec_verify_sample_workspace_bytes",
+           "specdec_tree_positions", "specdec_rope", "specdec_verify_tree_greedy", "specdec_verify_tree_sample",
+           "specdec_tree_compact", "specdec_tree_attention", "specdec_tree_attention_paged",
+           "specdec_tree_attention_workspace_bytes")
 
 
 class SpecDecError(RuntimeError):
@@ -78,6 +82,21 @@ def lib():
         L.specdec_pool_finish.argtypes = [C.POINTER(SeqBufC), C.POINTER(SchedC), vp, vp, ci, ci, C.c_int32, C.c_int32,
                                           vp, vp, vp, vp]
         L.specdec_pool_admit.argtypes = [C.POINTER(SeqBufC), C.POINTER(SchedC), C.POINTER(SeqBufC), vp, vp, vp, vp]
+        L.specdec_tree_positions.argtypes = [vp, ci, ci, vp, vp, ci, vp, vp, vp]
+        L.specdec_rope.argtypes = [vp, C.POINTER(i64), vp, C.POINTER(i64), ci, ci, ci, ci, ci, vp, vp, ci, ci, C.c_float,
+                                   vp]
+        L.specdec_verify_tree_greedy.argtypes = [vp, ci, i64, ci, ci, ci, vp, vp, ci, vp, vp, vp, vp, vp, sz, vp, vp]
+        L.specdec_verify_tree_sample.argtypes = [vp, ci, ci, ci, vp, vp, vp, vp, ci, vp, vp, vp, vp, sz, vp, vp]
+        L.specdec_tree_compact.argtypes = [vp, ci, ci, ci, ci, ci, ci, vp, vp, vp, ci, vp, vp, vp, vp]
+        L.specdec_tree_attention_workspace_bytes.argtypes = [ci, ci, ci, ci, ci]
+        L.specdec_tree_attention_workspace_bytes.restype = sz
+        L.specdec_tree_attention.argtypes = [C.POINTER(SeqBufC), vp, ci, ci, vp, C.POINTER(i64), ci, vp, vp, ci, ci,
+                                             C.c_float, vp, C.POINTER(i64), vp, sz, vp, vp]
+        L.specdec_tree_attention_paged.argtypes = [C.POINTER(PagedC), vp, ci, vp, C.POINTER(i64), ci, vp, vp, ci, ci,
+                                                   C.c_float, vp, C.POINTER(i64), vp, sz, vp, vp]
+        for f in ("specdec_tree_positions", "specdec_rope", "specdec_verify_tree_greedy", "specdec_verify_tree_sample",
+                  "specdec_tree_compact", "specdec_tree_attention", "specdec_tree_attention_paged"):
+            getattr(L, f).restype = C.c_int
         for f in ("specdec_workspace_init", "specdec_verify_greedy", "specdec_verify_greedy_noalloc",
                   "specdec_verify_sample",
                   "specdec_verify_sample_logits", "specdec_realign_kv", "specdec_group_by_len",
@@ -142,8 +161,8 @@ def _i32(shape, device):
     return torch.empty(shape, dtype=torch.int32, device=device)
 
 
-def _greedy_shape(logits, draft):
-    """(B, D, V, row_stride) of a greedy verification, after the tensor checks."""
+def _logit_rows(logits):
+    """(B, D, V, row_stride) of verified logits, after the tensor checks."""
     if logits.dtype not in _TORCH_DT or not logits.is_cuda or logits.dim() != 3:
         raise ValueError("logits must be a [B, D+1, V] float32/float16/bfloat16 device tensor")
     B, D1, V = logits.shape
@@ -156,6 +175,12 @@ def _greedy_shape(logits, draft):
         row_stride = logits.stride(1)
         if B > 1 and logits.stride(0) != D1 * row_stride:
             raise ValueError("logits rows must share one stride")
+    return B, D, V, row_stride
+
+
+def _greedy_shape(logits, draft):
+    """(B, D, V, row_stride) of a greedy verification, after the tensor checks."""
+    B, D, V, row_stride = _logit_rows(logits)
     _need(draft, "draft", torch.int32)
     if tuple(draft.shape) != (B, D):
         raise ValueError("draft must be [B, D]")
@@ -610,3 +635,286 @@ def pool_admit(pool, sched, queue, admitted=None, n_admitted=None, status=None):
                                   n_admitted.data_ptr(), _ptr(status), _stream())
     _check(rc, "specdec_pool_admit")
     return admitted, n_admitted
+
+
+# ---------------------------------------------------------- trees of drafts
+
+def _on(dev, *named):
+    """Every given tensor is on `dev` (the kernels dereference all of them there)."""
+    for t, n in named:
+        if t is not None and t.device != dev:
+            raise ValueError("%s must be on %s" % (n, dev))
+
+
+def _ints(shape, dev, *named):
+    """Required contiguous int32 tensors of one shape on `dev`."""
+    for t, n in named:
+        _need(t, n, torch.int32)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError("%s must have shape %s" % (n, list(shape)))
+    _on(dev, *named)
+
+
+def _launch(dev, name, *args):
+    """Calls entry point `name` on `dev`, on torch's current stream there."""
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if dev.index == torch.cuda.current_device():
+        rc = getattr(lib(), name)(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(lib(), name)(*args, stream)
+    _check(rc, name)
+
+
+def _depth(depth):
+    depth = int(depth)
+    if not 0 <= depth <= 255:
+        raise ValueError("depth must be in [0, 255]")
+    return depth
+
+
+def tree_positions(parent, lens, rows=None, pos=None, status=None):
+    """Positions [B, N] of the nodes of trees parent [B, N] whose rows hold lens
+    content positions (lens[rows[b]], or lens[b]): length plus depth, -1 for
+    nodes that are not used."""
+    _need(parent, "parent", torch.int32)
+    if parent.dim() != 2:
+        raise ValueError("parent must be [B, N]")
+    B, N = parent.shape
+    dev = parent.device
+    _need(lens, "lens", torch.int32)
+    if lens.dim() != 1 or (rows is None and lens.numel() < B):
+        raise ValueError("lens must hold one length per row")
+    _on(dev, (lens, "lens"))
+    if rows is not None:
+        _ints((B,), dev, (rows, "rows"))
+    pos = _i32((B, N), dev) if pos is None else _out(pos, "pos", B * N, device=dev)
+    _out(status, "status", 1, device=dev)
+    _launch(dev, "specdec_tree_positions", _ptr(parent), B, N, _ptr(lens), _ptr(rows), lens.numel(), _ptr(pos),
+            _ptr(status))
+    return pos
+
+
+def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=None, fast=32.0, slow=1.0, device="cuda"):
+    """Frequencies (fp64 [rot/2], radians per position) and the factor of `rope`.
+
+    scaling None: base**(-2k/rot).  For contexts `factor` times as long as the
+    model was trained on: "linear" divides every frequency by it; "ntk" raises the
+    base, to base * factor**(rot/(rot-2)), so that the slowest pair slows by
+    `factor` and the fastest keeps its pace; "parts" (arXiv 2309.00071) leaves pairs that turn
+    more than `fast` times over the `original` context, divides those that turn less
+    than `slow` times, ramps between, and sharpens the scores by a factor of
+    0.1 ln(factor) + 1 on both sides."""
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and positive")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    k = torch.arange(rot // 2, dtype=torch.float64)
+    freq, attn = float(base) ** (-2.0 * k / rot), 1.0
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "ntk":
+        if rot == 2:
+            raise ValueError("ntk scaling needs more than one pair")
+        freq = (float(base) * float(factor) ** (rot / (rot - 2.0))) ** (-2.0 * k / rot)
+    elif scaling == "parts":
+        if original is None or not original > 0 or not fast > slow:
+            raise ValueError("parts scaling needs the original context and fast > slow")
+        turns = freq * (original / (2.0 * math.pi))
+        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
+        freq = freq * keep + freq / factor * (1.0 - keep)
+        attn = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+    elif scaling is not None:
+        raise ValueError("scaling must be None, 'linear', 'ntk' or 'parts'")
+    return freq.to(device), attn
+
+
+def _heads_view(t, name):
+    """A [B, N, heads, Dh] device tensor whose heads are contiguous: its strides."""
+    if t.dim() != 4 or t.dtype not in _TORCH_DT or not t.is_cuda:
+        raise ValueError("%s must be a [B, N, heads, Dh] float32/float16/bfloat16 device tensor" % name)
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError("%s must have a contiguous last dimension" % name)
+    return (C.c_int64 * 3)(*t.stride()[:3])
+
+
+def rope(x, pos, freq, interleaved=False, factor=1.0, out=None):
+    """Rotary positions: the first 2 * len(freq) elements of every head of x
+    [B, N, heads, Dh] (strided; heads contiguous) turn by pos [B, N] * freq (fp64,
+    see rope_frequencies).  Tokens with a negative position are left as they are
+    in `out`: x itself to work in place, or a new tensor by default, which holds
+    no values there.  Returns out."""
+    xs = _heads_view(x, "x")
+    B, N, H, Dh = x.shape
+    dev = x.device
+    _ints((B, N), dev, (pos, "pos"))
+    _need(freq, "freq", torch.float64)
+    if freq.dim() != 1:
+        raise ValueError("freq must be one-dimensional")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and type")
+    os_ = _heads_view(out, "out")
+    _on(dev, (freq, "freq"), (out, "out"))
+    _launch(dev, "specdec_rope", _ptr(x), xs, _ptr(out), os_, _TORCH_DT[x.dtype], B, N, H, Dh, _ptr(pos), _ptr(freq),
+            2 * freq.numel(), int(bool(interleaved)), float(factor))
+    return out
+
+
+def verify_tree_greedy(logits, draft, parent, depth, ws=None, status=None, accept_len=None, next_token=None, path=None,
+                       target_tok=None):
+    """Greedy verification of trees of drafts: logits [B, N, V] (strided as for
+    verify_greedy), draft and parent [B, N], at most `depth` accepted.  The
+    workspace is workspace(B, N - 1).  Returns (accept_len [B], next_token [B],
+    path [B, depth+1])."""
+    B, D, V, row_stride = _logit_rows(logits)
+    N = D + 1
+    if N < 1:
+        raise ValueError("a tree has one node at least")
+    dev = logits.device
+    depth = _depth(depth)
+    _ints((B, N), dev, (draft, "draft"), (parent, "parent"))
+    accept_len = _i32(B, dev) if accept_len is None else _out(accept_len, "accept_len", B, device=dev)
+    next_token = _i32(B, dev) if next_token is None else _out(next_token, "next_token", B, device=dev)
+    path = _i32((B, depth + 1), dev) if path is None else _out(path, "path", B * (depth + 1), device=dev)
+    _out(target_tok, "target_tok", B * N, device=dev)
+    _out(status, "status", 1, device=dev)
+    if ws is None:
+        with torch.cuda.device(dev):
+            ws = workspace(B, N - 1, dev)
+    else:
+        _out(ws, "ws", 1, torch.uint8, device=dev)
+    _launch(dev, "specdec_verify_tree_greedy", _ptr(logits), _TORCH_DT[logits.dtype], row_stride, B, N, V, _ptr(draft),
+            _ptr(parent), depth, _ptr(accept_len), _ptr(next_token), _ptr(path), _ptr(target_tok), _ptr(ws), ws.numel(),
+            _ptr(status))
+    return accept_len, next_token, path
+
+
+def verify_tree_sample(p, draft, parent, u_accept, u_draw, depth, ws=None, status=None, accept_len=None,
+                       next_token=None, path=None):
+    """Sampled verification of trees of drafts from the target's probabilities p
+    [B, N, V] (float32) and uniforms u_accept, u_draw [B, N], at most `depth`
+    accepted.  The workspace is sample_verify_workspace(B, N - 1, V).  Returns
+    (accept_len [B], next_token [B], path [B, depth+1])."""
+    _need(p, "p", torch.float32)
+    if p.dim() != 3 or p.shape[1] < 1:
+        raise ValueError("p must be [B, N, V]")
+    B, N, V = p.shape
+    dev = p.device
+    depth = _depth(depth)
+    _ints((B, N), dev, (draft, "draft"), (parent, "parent"))
+    for t, n in ((u_accept, "u_accept"), (u_draw, "u_draw")):
+        _need(t, n, torch.float32)
+        if tuple(t.shape) != (B, N):
+            raise ValueError("%s must be [B, N]" % n)
+        _on(dev, (t, n))
+    accept_len = _i32(B, dev) if accept_len is None else _out(accept_len, "accept_len", B, device=dev)
+    next_token = _i32(B, dev) if next_token is None else _out(next_token, "next_token", B, device=dev)
+    path = _i32((B, depth + 1), dev) if path is None else _out(path, "path", B * (depth + 1), device=dev)
+    _out(status, "status", 1, device=dev)
+    if ws is None and B > 0:
+        with torch.cuda.device(dev):
+            ws = sample_verify_workspace(B, N - 1, V, dev)
+    elif ws is not None:
+        _out(ws, "ws", 1, torch.uint8, device=dev)
+    _launch(dev, "specdec_verify_tree_sample", _ptr(p), B, N, V, _ptr(draft), _ptr(parent), _ptr(u_accept), _ptr(u_draw),
+            depth, _ptr(accept_len), _ptr(next_token), _ptr(path), _ptr(ws), 0 if ws is None else ws.numel(),
+            _ptr(status))
+    return accept_len, next_token, path
+
+
+def tree_compact(kv_new, draft, path, accept_len, kv_path=None, draft_path=None, status=None):
+    """The accepted path's KV entries and token ids as a chain's round leaves them:
+    kv_new [L, 2, B, H, N, Dh], draft [B, N], path [B, depth+1] and accept_len [B]
+    give (kv_path [L, 2, B, H, depth+1, Dh], draft_path [B, depth]), which the
+    appends and realignments take.  Entries past accept_len are not written."""
+    _need(kv_new, "kv_new")
+    if kv_new.dim() != 6 or kv_new.shape[1] != 2 or kv_new.dtype not in _TORCH_DT:
+        raise ValueError("kv_new must be a [L, 2, B, H, N, Dh] float32/float16/bfloat16 tensor")
+    L, _, B, H, N, Dh = kv_new.shape
+    dev = kv_new.device
+    _need(path, "path", torch.int32)
+    if path.dim() != 2 or path.shape[0] != B or path.shape[1] < 1:
+        raise ValueError("path must be [B, depth+1]")
+    depth = _depth(path.shape[1] - 1)
+    _ints((B, N), dev, (draft, "draft"))
+    _ints((B,), dev, (accept_len, "accept_len"))
+    _on(dev, (path, "path"))
+    shape = (L, 2, B, H, depth + 1, Dh)
+    if kv_path is None:
+        kv_path = torch.empty(shape, dtype=kv_new.dtype, device=dev)
+    else:
+        _need(kv_path, "kv_path", kv_new.dtype)
+        if tuple(kv_path.shape) != shape:
+            raise ValueError("kv_path must be [L, 2, B, H, depth+1, Dh]")
+        _on(dev, (kv_path, "kv_path"))
+    draft_path = _i32((B, depth), dev) if draft_path is None else _out(draft_path, "draft_path", B * depth, device=dev)
+    _out(status, "status", 1, device=dev)
+    _launch(dev, "specdec_tree_compact", _ptr(kv_new), _TORCH_DT[kv_new.dtype], L, B, H, N, Dh, _ptr(draft), _ptr(path),
+            _ptr(accept_len), depth, _ptr(kv_path), _ptr(draft_path), _ptr(status))
+    return kv_path, draft_path
+
+
+def tree_attention_workspace(B, N, q_heads, kv_heads, head_dim, device="cuda"):
+    """A cleared workspace of tree_attention, for any batch and cache with this N,
+    q_heads / kv_heads and head_dim, on one stream."""
+    dev = torch.device(device)
+    if dev.index is None:
+        dev = torch.device(dev.type, torch.cuda.current_device())
+    with torch.cuda.device(dev):
+        n = int(lib().specdec_tree_attention_workspace_bytes(B, N, q_heads, kv_heads, head_dim))
+        if n == 0:
+            raise SpecDecError(E_ARG, "specdec_tree_attention_workspace_bytes")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        _check(lib().specdec_workspace_init(ws.data_ptr(), n, _stream()), "specdec_workspace_init")
+    return ws
+
+
+def tree_attention(q, cache, layer, kv_new, parent, rows=None, group=0, scale=None, out=None, ws=None, status=None):
+    """Attention of the nodes of trees parent [B, N] over one layer of `cache` (a
+    PagedKV, a SeqBuf rectangle, or a SeqBuf pool) and over each node's ancestors
+    and itself, whose keys and values are kv_new [L, 2, B, H, N, Dh].
+
+    q [B, N, q_heads, Dh] (strided; heads contiguous) in the cache's type; query
+    head h reads KV head h // (q_heads // H).  rows [B] names the cache rows of a
+    PagedKV or pool (default b); `group` is a GATHER rectangle's rows per group.
+    scale defaults to Dh**-0.5.  Nodes outside the tree are left as they are in
+    `out` (a new tensor by default, which holds no values there).  Returns out."""
+    qs = _heads_view(q, "q")
+    B, N, Hq, Dh = q.shape
+    dev = q.device
+    paged = isinstance(cache, PagedKV)
+    if not paged and not isinstance(cache, SeqBuf):
+        raise ValueError("cache must be a PagedKV or a SeqBuf")
+    kv = cache.pages if paged else cache.kv
+    L, H = kv.shape[0], kv.shape[3]
+    if kv.shape[5] != Dh or q.dtype != kv.dtype:
+        raise ValueError("q must have the cache's head size and type")
+    _need(kv_new, "kv_new", kv.dtype)
+    if tuple(kv_new.shape) != (L, 2, B, H, N, Dh):
+        raise ValueError("kv_new must be [L, 2, B, H, N, Dh] of the cache's geometry")
+    _ints((B, N), dev, (parent, "parent"))
+    if rows is not None:
+        _ints((B,), dev, (rows, "rows"))
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and type")
+    os_ = _heads_view(out, "out")
+    _on(dev, (kv, "cache"), (kv_new, "kv_new"), (out, "out"))
+    group = int(group)
+    if not paged and group > 0 and cache.width is not None and cache.width.numel() * group < B:
+        raise ValueError("the rectangle's width tensor needs one entry per group")
+    _out(status, "status", 1, device=dev)
+    if ws is None:
+        if B == 0:
+            return out
+        ws = tree_attention_workspace(B, N, Hq, H, Dh, dev)
+    else:
+        _out(ws, "ws", 1, torch.uint8, device=dev)
+    scale = Dh ** -0.5 if scale is None else float(scale)
+    head = (C.byref(cache.c), _ptr(rows)) if paged else (C.byref(cache.c), _ptr(rows), group)
+    _launch(dev, "specdec_tree_attention_paged" if paged else "specdec_tree_attention", *head, int(layer), _ptr(q), qs, Hq,
+            _ptr(kv_new), _ptr(parent), B, N, scale, _ptr(out), os_, _ptr(ws), ws.numel(), _ptr(status))
+    return out

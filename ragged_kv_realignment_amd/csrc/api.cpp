@@ -800,27 +800,45 @@ EXPORT int specdec_tree_compact(const void *kv_new, int dtype, int layers, int B
 
 // Query tiles by the number of query rows M = N * Hq / Hkv of a KV head: few
 // rows leave all four waves to the keys; more rows go to more tiles per wave,
-// then to more waves.
+// then to more waves, which leave fewer for the keys.
 namespace sd {
 AttnShape attn_shape(int dtype, int Dh, int M) {
   AttnShape a;
   a.dhp = Dh <= 64 ? 64 : Dh <= 128 ? 128 : 256;
-  const int most = attn_most_tiles(dtype, a.dhp), tiles = (M + 15) / 16;
-  if (tiles <= most) {
+  const int most = attn_most_tiles(dtype, a.dhp);
+  if (M <= 16 * most) {
+    a.rt = M <= 16 ? 1 : 2;
     a.rw = 1;
-    a.rt = tiles == 3 ? 4 : tiles;
+    a.kw = 4;
+    return a;
+  }
+  const bool wide = attn_waves_per_simd(dtype, a.dhp) == 1;  // fp32 heads over 128
+  a.kw = 1;
+  a.rt = 1;
+  if (wide || M <= 64) {
+    a.rw = 4;
+    a.kw = wide ? 1 : 2;
+  } else if (most == 2 && (M <= 96 || (M > 128 && M <= 192))) {
+    a.rw = 6;  // blocks of 96 rows: the least rows left over
   } else {
-    a.rw = tiles <= 2 * most ? 2 : 4;
-    a.rt = a.rw == 2 && most >= 4 && tiles <= 6 ? 3 : most;
+    a.rw = 8;
+    a.rt = most == 2 && M > 128 ? 2 : 1;
   }
   return a;
 }
 
-// Workgroups of a launch: what fits the CUs at once.
-int attn_grid(const AttnShape &a) {
-  return (device_cus() * attn_wgs_per_cu(a.rt, a.dhp) + 7) / 8 * 8;
+// Workgroups that the device holds at once.
+int attn_resident(int dtype, const AttnShape &a) {
+  return device_cus() * (4 * attn_waves_per_simd(dtype, a.dhp) / (a.rw * a.kw) > 1 ? 2 : 1);
 }
 }  // namespace sd
+
+// A segment in several parts has less than two parts per resident workgroup's
+// share of the work, so all of them have less than twice the resident ones.
+static size_t attn_workspace(int dtype, const sd::AttnShape &a, size_t &slots) {
+  slots = 2 * (size_t)sd::attn_resident(dtype, a);
+  return slots * (sd::kAtomicLine + a.part_bytes());
+}
 
 EXPORT size_t specdec_tree_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, int head_dim) {
   if (!tree_shape_ok(B, N, 0) || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads || head_dim < 1 ||
@@ -829,7 +847,8 @@ EXPORT size_t specdec_tree_attention_workspace_bytes(int B, int N, int q_heads, 
   size_t most = 0;
   for (int dt = 0; dt < 3; ++dt) {
     const sd::AttnShape a = sd::attn_shape(dt, head_dim, N * (q_heads / kv_heads));
-    const size_t n = (size_t)sd::attn_grid(a) * (sd::kAtomicLine + a.wg_bytes());
+    size_t slots;
+    const size_t n = attn_workspace(dt, a, slots);
     most = n > most ? n : most;
   }
   return most;
@@ -871,9 +890,15 @@ static int attention(sd::TreeAttnParams &p, const void *kv, size_t old_bytes, in
       overlap(op, on, p.len, (size_t)p.n_rows * 4) || overlap(op, on, ws, ws_bytes))
     return SPECDEC_E_ALIAS;
   const sd::AttnShape a = sd::attn_shape(dtype, Dh, N * p.G);
-  p.grid = sd::attn_grid(a);
-  const size_t counters = (size_t)p.grid * sd::kAtomicLine, partial = (size_t)p.grid * a.wg_bytes();
-  if (!ws || ws_bytes < counters + partial || reinterpret_cast<uintptr_t>(ws) % 16 != 0) return SPECDEC_E_WORKSPACE;
+  p.blocks = (N * p.G + a.rows() - 1) / a.rows();
+  p.resident = sd::attn_resident(dtype, a);
+  const long long segs = (long long)B * H * p.blocks;
+  if (segs >= (1LL << 30)) return SPECDEC_E_ARG;
+  p.grid = (int)(segs < p.resident ? p.resident : segs + p.resident + 7) / 8 * 8;
+  if (p.grid < p.resident) p.grid += 8;
+  size_t slots;
+  const size_t need = attn_workspace(dtype, a, slots), counters = slots * sd::kAtomicLine, partial = need - counters;
+  if (!ws || ws_bytes < need || reinterpret_cast<uintptr_t>(ws) % 16 != 0) return SPECDEC_E_WORKSPACE;
   if (partial >= (1u << 31)) return SPECDEC_E_ARG;
   p.q = q;
   p.out = out;
@@ -883,7 +908,10 @@ static int attention(sd::TreeAttnParams &p, const void *kv, size_t old_bytes, in
   }
   p.k_new = nk;
   p.v_new = nk + half;
-  p.scale = (float)((double)scale * 1.44269504088896340736);  // log2(e): the kernel's exponentials are of base 2
+  // the kernel's exponentials are of base 2; a masked score is -inf, which a
+  // scale of 0 would turn into NaN: the smallest normal number stands for it
+  p.scale = fmaxf((float)(fabs((double)scale) * 1.44269504088896340736), 1.17549435e-38f);
+  p.negate = scale < 0.0f;
   p.counters = static_cast<unsigned int *>(ws);
   p.partial = static_cast<char *>(ws) + counters;
   p.partial_bytes = (int)partial;

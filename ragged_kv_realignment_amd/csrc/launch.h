@@ -44,23 +44,23 @@ constexpr int kRopeTokens = 16;          // tokens one rotary workgroup turns at
 // Tree attention.
 constexpr int kMaxAttnRows = 1024;       // batch rows (their lengths' prefix sums are kept in LDS)
 
-// Query rows of a workgroup: rw waves of rt 16-row tiles, the other 4 / rw waves
-// taking other keys; the head size is padded to dhp.
+// Query rows of a workgroup: rw waves of rt 16-row tiles, times kw waves that
+// take other keys; the head size is padded to dhp.
 struct AttnShape {
-  int dhp, rt, rw;
+  int dhp, rt, rw, kw;
   int rows() const { return rw * rt * 16; }
-  // partial results of one workgroup (two segments at most): per query row O, then max and sum
-  size_t wg_bytes() const { return (size_t)2 * rows() * (dhp + 4) * 4; }
+  // a part's results in the workspace: per query row O, then max and sum
+  size_t part_bytes() const { return (size_t)rows() * (dhp + 4) * 4; }
 };
 
-// 16-row query tiles a wave can hold beside its keys in 512 registers.
-constexpr int attn_most_tiles(int dtype, int dhp) {
-  return dtype == 0 ? (dhp == 256 ? 1 : 2) : (dhp == 256 ? 2 : 4);
-}
-// Workgroups per CU that the registers and LDS of an instance are held to.
-constexpr int attn_wgs_per_cu(int rt, int dhp) { return rt <= 2 && dhp <= 128 ? 2 : 1; }
+// Waves per SIMD, and 16-row query tiles that a wave can hold beside its keys in
+// the registers that leaves (256, or 512 for fp32 heads over 128).
+constexpr int attn_waves_per_simd(int dtype, int dhp) { return dtype == 0 && dhp == 256 ? 1 : 2; }
+// Tiles in LDS of a stage's bytes: at most six, in 128 KiB.
+constexpr int attn_stages(int bytes) { return 131072 / bytes > 6 ? 6 : 131072 / bytes; }
+constexpr int attn_most_tiles(int dtype, int dhp) { return dhp * (dtype == 0 ? 2 : 1) <= 128 ? 2 : 1; }
 AttnShape attn_shape(int dtype, int Dh, int M);
-int attn_grid(const AttnShape &a);
+int attn_resident(int dtype, const AttnShape &a);  // workgroups that the device holds at once
 
 struct TreeAttnParams {
   const void *q;                         // strided (row, node, query head), Dh contiguous
@@ -74,10 +74,11 @@ struct TreeAttnParams {
   int n_rows, cap, group;
   const int32_t *parent;                 // [B][N]
   int B, N, H, G, Dh;
-  float scale;                           // times log2(e)
+  float scale;                           // its size times log2(e)
+  bool negate;                           // it was negative
   unsigned int *counters;                // workspace: a line per workgroup, zero between calls
   void *partial;
-  int partial_bytes, grid;
+  int partial_bytes, blocks, resident, grid;  // query blocks per head, workgroups
   int32_t *status;
   FastDiv page_div, g_div;
 };

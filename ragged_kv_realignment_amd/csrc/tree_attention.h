@@ -25,25 +25,27 @@
 // mantissa for bf16): their errors average over the keys to less than the
 // output's own rounding.
 //
-// Work split.  Rows have ragged lengths, so the key tiles of all (row, KV head,
-// query block) segments are laid end to end and every workgroup takes an equal
-// run of them (in units of one tile per key wave), whatever segments that
-// crosses.  A segment within one workgroup is finished there; otherwise its
-// workgroups leave (max, sum, O) in the workspace and the last to arrive adds
-// them in workgroup order, so results do not depend on timing.  The order of
-// completion uses the same scheme as verification: sums stored past the
-// non-coherent L2 (sc1), completed (vmcnt) before the count, loaded only after
-// the count has returned.
+// Up to eight waves share the queries of a block (more rows per workgroup) or the
+// keys of a segment (few rows).  Waves that share keys take them through LDS.
+//
+// A segment that is cut into parts (see plan) leaves (max, sum, O) of each in the
+// workspace, and the last workgroup to arrive adds them in part order, so results
+// do not depend on timing.  The order of completion uses the same scheme as
+// verification: sums stored past the non-coherent L2 (sc1), completed (vmcnt)
+// before the count, loaded only after the count has returned.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "coherent.h"
 #include "device_common.h"
 #include "launch.h"
 #include "specdec.h"
 #include "tree_common.h"
+#include "wave_dpp.h"
 
 namespace sd {
 
@@ -55,10 +57,10 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
 constexpr int kTile = 32;        // keys of a wave's step
 constexpr float kSlack = 8.0f;   // log2 of the largest weight before the maximum is raised
+constexpr int kWindow = 1024;       // page ids in LDS
+constexpr uint32_t kMinUnits = 4; // of a part (see plan)
 constexpr float kLow = -1e30f;   // running maximum before the first key
 
 template <int DT> constexpr int es() { return DT == 0 ? 4 : 2; }
@@ -119,36 +121,6 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   }
 }
 
-// Inclusive prefix sums of n <= NT * 4 values into pre[1..n], pre[0] = 0.
-template <typename F>
-__device__ __forceinline__ void block_prefix(int n, long long *pre, long long *scratch, F value) {
-  const int per = (n + kThreads - 1) / kThreads, t = threadIdx.x, lane = t & (kWave - 1);
-  long long own = 0;
-  for (int k = 0; k < per; ++k) {
-    const int i = t * per + k;
-    if (i < n) own += value(i);
-  }
-  long long incl = own;
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const long long y = __shfl_up(incl, off);
-    if (lane >= off) incl += y;
-  }
-  if (lane == kWave - 1) scratch[t / kWave] = incl;
-  __syncthreads();
-  long long run = incl - own;
-  for (int k = 0; k < t / kWave; ++k) run += scratch[k];
-  for (int k = 0; k < per; ++k) {
-    const int i = t * per + k;
-    if (i < n) {
-      run += value(i);
-      pre[i + 1] = run;
-    }
-  }
-  if (t == 0) pre[0] = 0;
-  __syncthreads();
-}
-
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // 16-byte stores and loads of partial sums through the coherence point.
@@ -157,11 +129,6 @@ __device__ __forceinline__ void st_f4(__amdgpu_buffer_rsrc_t r, uint32_t off, f3
 }
 __device__ __forceinline__ f32x4 ld_f4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kCoherentPolicy));
-}
-
-// The workgroup whose run [total w / W, total (w + 1) / W) holds unit x.
-__device__ __forceinline__ int first_wg(long long x, long long total, int W) {
-  return (int)(((x + 1) * W - 1) / total);
 }
 
 // Elements e .. e+7 (a, then d) of query row `row` of (b, h), unless its node
@@ -203,134 +170,324 @@ __device__ __forceinline__ void add_odd(const TreeAttnParams &p, const char *v, 
 
 }  // namespace
 
-// RT 16-query tiles per wave, RW waves across query blocks, KW = 4 / RW waves
-// across keys; DHP the head size, or with PAD the next of 64, 128 and 256.
-template <int DT, int DHP, int RT, int RW, bool PAD>
-__global__ __launch_bounds__(kThreads, attn_wgs_per_cu(RT, DHP)) void k_tree_attention(TreeAttnParams p) {
-  constexpr int KW = kWaves / RW;
+namespace {
+
+// Ancestor bits of every node (itself included) from its raw parent, a node per
+// thread, by pointer doubling in LDS: after round k a node holds the bits of 2^k
+// generations and the pointer past them.  A node outside the tree gets none.
+__device__ __forceinline__ void tree_ancestors(int N, int raw, int32_t *status, int *ptr,
+                                               uint32_t (*anc)[kMaxNodes / 32]) {
+  const int t = threadIdx.x, words = (N + 31) / 32;
+  bool bad = false;
+  if (t < N) {
+    ptr[t] = node_parent(t, raw, bad);
+    for (int k = 0; k < words; ++k) anc[t][k] = (t >> 5) == k ? 1u << (t & 31) : 0u;
+  }
+  if (bad) set_status(status, SPECDEC_S_TREE);
+  for (int span = 1; span < N; span <<= 1) {
+    __syncthreads();
+    int q = 0;
+    uint32_t up[kMaxNodes / 32] = {};
+    if (t < N) {
+      q = ptr[t];
+      if (q > 0) {
+        for (int k = 0; k < words; ++k) up[k] = anc[q][k];
+        q = ptr[q];
+      }
+    }
+    __syncthreads();
+    if (t < N) {
+      ptr[t] = q;
+      for (int k = 0; k < words; ++k) anc[t][k] |= up[k];
+    }
+  }
+  if (t < N) {
+    for (int k = 0; k < words; ++k) anc[t][k] = ptr[t] < 0 ? 0u : k == 0 ? anc[t][k] | 1u : anc[t][k];
+  }
+  __syncthreads();
+}
+
+// Loads that write LDS directly: lane i's 16 bytes go to `to` (the same in all
+// lanes) + 16 i.
+__device__ __forceinline__ void load_lds(const void *from, void *to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                   (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+}
+__device__ __forceinline__ uint32_t lds_offset(const void *p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+// At most N of this wave's loads are still out (they return in order); N is
+// rounded down to what the instruction can say.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N > 63 ? 63 : N) : "memory");
+}
+__device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Reads of LDS that those loads have written, waited for here.  As ordinary
+// loads the compiler would have each of them wait for every load to LDS that is
+// out, the next tiles' too.
+template <int OFF>
+__device__ __forceinline__ void lds_read(u32x4 &a, u32x4 &b, u32x4 &c, u32x4 &d, uint32_t p, uint32_t q) {
+  asm volatile(
+      "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %4 offset:%6\n\tds_read_b128 %3, %5 offset:%6\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
+      : "v"(p), "v"(q), "n"(OFF)
+      : "memory");
+}
+// The rows at q, r and s lie ROW, 2 ROW and 3 ROW bytes on.
+template <int OFF, int ROW, int>
+__device__ __forceinline__ void lds_read(u32x4 &a, u32x4 &b, u32x4 &c, u32x4 &d, u32x4 &e, u32x4 &f, u32x4 &g, u32x4 &h,
+                                         uint32_t p, uint32_t q, uint32_t r, uint32_t s) {
+  asm volatile(
+      "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9 offset:%12\n\tds_read_b128 %2, %10 offset:%13\n\t"
+      "ds_read_b128 %3, %11 offset:%14\n\tds_read_b128 %4, %8 offset:%15\n\tds_read_b128 %5, %9 offset:%16\n\t"
+      "ds_read_b128 %6, %10 offset:%17\n\tds_read_b128 %7, %11 offset:%18\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h)
+      : "v"(p), "v"(q), "v"(r), "v"(s), "n"(ROW), "n"(2 * ROW), "n"(3 * ROW), "n"(OFF), "n"(OFF + ROW), "n"(OFF + 2 * ROW),
+        "n"(OFF + 3 * ROW)
+      : "memory");
+}
+template <int OFF, int ROW, int>
+__device__ __forceinline__ void lds_read(u32x2 &a, u32x2 &b, u32x2 &c, u32x2 &d, u32x2 &e, u32x2 &f, u32x2 &g, u32x2 &h,
+                                         uint32_t p, uint32_t q, uint32_t r, uint32_t s) {
+  asm volatile(
+      "ds_read_b64 %0, %8\n\tds_read_b64 %1, %9 offset:%12\n\tds_read_b64 %2, %10 offset:%13\n\t"
+      "ds_read_b64 %3, %11 offset:%14\n\tds_read_b64 %4, %8 offset:%15\n\tds_read_b64 %5, %9 offset:%16\n\t"
+      "ds_read_b64 %6, %10 offset:%17\n\tds_read_b64 %7, %11 offset:%18\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h)
+      : "v"(p), "v"(q), "v"(r), "v"(s), "n"(ROW), "n"(2 * ROW), "n"(3 * ROW), "n"(OFF), "n"(OFF + ROW), "n"(OFF + 2 * ROW),
+        "n"(OFF + 3 * ROW)
+      : "memory");
+}
+
+// Words of LDS, beside loads to LDS that are out.
+__device__ __forceinline__ uint32_t lds_get(uint32_t at) {
+  uint32_t v;
+  asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void lds_set(uint32_t at, uint32_t v) {
+  asm volatile("ds_write_b32 %0, %1" ::"v"(at), "v"(v) : "memory");
+}
+
+// How the pieces of a row of P are turned among its slots in LDS (256 bytes are
+// all banks: two rows of 8 pieces, or 16 pieces of a longer row).
+template <int P>
+__device__ __forceinline__ int swz(int row) {
+  return P == 8 ? (row >> 1) & 7 : row & 15;
+}
+
+// Waits for the queries, here instead of with every use in a loop (where the
+// wait would cover the keys on their way), and flips their signs where the scale
+// was negative.
+template <int DT, int RT, int KS>
+__device__ __forceinline__ void settle(u32x4 (&q)[RT][KS], bool negate) {
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int s = 0; s < KS; ++s) asm volatile("" : "+v"(q[rt][s]));
+  if (!negate) return;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int s = 0; s < KS; ++s) q[rt][s] ^= (u32x4)(DT == 0 ? 0x80000000u : 0x80008000u);
+}
+
+// What one workgroup does: units [unit0, unit1) (of KW key tiles) of segment
+// `seg` (head x query block) of batch row b; as the part of a segment in several
+// parts, its slot in the workspace, the segment's first slot and its parts.
+struct Chunk {
+  int b, seg, row, len, start;
+  int unit0, unit1;
+  int slot, slot0, parts;  // slot -1: the whole segment
+};
+
+// The split.  A segment (batch row, KV head, query block) is cut into parts of at
+// most `u` units, and a workgroup takes one part: a part ends in about 4 us of
+// sums, stores and joins, so no workgroup takes pieces of two segments.
+//  - With fewer segments than resident workgroups, u is about the least for which
+//    every part gets a resident workgroup (the estimate counts half a part lost
+//    per segment, and grows by an eighth until the parts fit).
+//  - With more, u is a resident workgroup's share of the work: long rows are cut
+//    to it, the others stay whole, and the launch runs them as places fall free.
+//  - Parts under kMinUnits gain nothing.
+// Every wave works it out by itself from the lengths, 64 rows at a time, a row per
+// lane, in doubles (exact below 2^53) for their lane scans.  Returns false where
+// there is nothing for this workgroup.
+template <int KW>
+__device__ __forceinline__ bool plan(const TreeAttnParams &p, int HR, int tree_tiles, Chunk &k) {
+  const int lane = threadIdx.x & (kWave - 1);
+  struct Row {
+    int row, len, start;
+    bool bad;
+    uint32_t units;
+  };
+  auto load = [&](int b0) {
+    Row x{};
+    const int b = b0 + lane;
+    if (b < p.B) {
+      x.row = p.rows ? p.rows[b] : b;
+      const bool in = x.row >= 0 && x.row < p.n_rows;
+      x.len = in ? p.len[x.row] : -1;
+      x.start = p.width ? p.width[p.group > 0 ? b / p.group : 0] - x.len : 0;
+      x.bad = x.len < 0 || x.start < 0 || (long long)x.start + x.len > p.cap;
+      x.units = x.bad ? 0u : (uint32_t)(((x.len + kTile - 1) / kTile + tree_tiles + KW - 1) / KW);
+    }
+    return x;
+  };
+  Row one = load(0);  // all there is for B <= 64
+  double total = 0.0;
+  uint32_t longest = 0;
+  bool bad = false;
+  for (int b0 = 0; b0 < p.B; b0 += kWave) {
+    const Row x = b0 ? load(b0) : one;
+    bad |= x.bad;
+    total += wave_total_f64((double)x.units);
+    longest = max(longest, x.units);
+  }
+  longest = (uint32_t)wave_max_f32((float)longest) + 1u;  // an upper bound (fp32 may round down by less than one in 2^24)
+  longest += longest >> 20;
+  const double segs = (double)p.B * HR;
+  bad = __any(bad);
+  if (bad || total * HR >= 2147483648.0) {
+    if (threadIdx.x == 0) set_status(p.status, SPECDEC_S_LEN_RANGE);
+    return false;
+  }
+  const double room = p.resident > segs ? (double)p.resident - 0.5 * segs : (double)p.resident;
+  uint32_t u = (uint32_t)(total * HR / room) + 1u;
+  u = u < kMinUnits ? kMinUnits : u;
+  auto parts = [&](uint32_t units) { return (units + u - 1) / u; };
+  if (p.resident > segs) {
+    for (int k = 0; u < longest; ++k) {
+      double n = 0.0;
+      for (int b0 = 0; b0 < p.B; b0 += kWave) n += wave_total_f64((double)parts((b0 ? load(b0) : one).units));
+      if (n * HR <= p.resident) break;
+      u = k < 16 ? u + (u + 7) / 8 : longest;
+    }
+  }
+  // all parts, in order of batch row, segment and key; those of cut segments have slots
+  double all = 0.0;
+  for (int b0 = 0; b0 < p.B; b0 += kWave) all += wave_total_f64((double)parts((b0 ? load(b0) : one).units));
+  const int W = (int)(all * HR);
+  // consecutive parts on one XCD (workgroups go to the 8 XCDs in turn), so query
+  // blocks that share keys share an L2
+  const int per_xcd = (W + 7) / 8, on_xcd = (int)(blockIdx.x >> 3);
+  const int w = (int)(blockIdx.x & 7) * per_xcd + on_xcd;
+  if (on_xcd >= per_xcd || w >= W) return false;
+  double before = 0.0, slots = 0.0;
+  for (int b0 = 0; b0 < p.B; b0 += kWave) {
+    const Row x = b0 ? load(b0) : one;
+    const uint32_t n = parts(x.units);
+    const double mine = (double)n * HR, cut = n > 1 ? mine : 0.0;
+    const double incl = wave_scan_f64(mine), icut = wave_scan_f64(cut);
+    const unsigned long long hit = __ballot(before + incl > w);
+    if (hit) {
+      const int at = __builtin_ctzll(hit);
+      k.b = b0 + at;
+      k.row = __builtin_amdgcn_readlane(x.row, at);
+      k.len = __builtin_amdgcn_readlane(x.len, at);
+      k.start = __builtin_amdgcn_readlane(x.start, at);
+      const int units = __builtin_amdgcn_readlane((int)x.units, at), np = __builtin_amdgcn_readlane((int)n, at);
+      const int rel = w - (int)(before + lane_f64(incl - mine, at));
+      k.seg = rel / np;
+      const int part = rel - k.seg * np;
+      // even parts: the first `units % np` are one longer
+      const int each = units / np, longer = units - each * np;
+      k.unit0 = part * each + min(part, longer);
+      k.unit1 = k.unit0 + each + (part < longer);
+      k.parts = np;
+      k.slot0 = np > 1 ? (int)(slots + lane_f64(icut - cut, at)) + k.seg * np : 0;
+      k.slot = np > 1 ? k.slot0 + part : -1;
+      return true;
+    }
+    before += lane_f64(incl, kWave - 1);
+    slots += lane_f64(icut, kWave - 1);
+  }
+  return false;
+}
+
+}  // namespace
+
+// RT 16-query tiles per wave, RW waves across queries times KW across keys; DHP
+// the head size, or with PAD the next of 64, 128 and 256.
+template <int DT, int DHP, int RT, int RW, int KW, bool PAGED, bool PAD>
+__global__ __launch_bounds__(RW * KW * kWave, attn_waves_per_simd(DT, DHP)) void k_tree_attention(TreeAttnParams p) {
+  constexpr int NW = RW * KW, NT = NW * kWave;
+  constexpr bool SHARED = RW > 1;         // keys pass through LDS, for the waves that share them
+  constexpr bool NEXT = !SHARED && RT == 1;
   constexpr int ES = es<DT>();
   constexpr int EL = 16 / ES;             // elements of a 16-byte piece
   constexpr int KS = DHP / (4 * EL);      // contraction steps of S (4 lane groups x EL elements)
   constexpr int NE = DHP / 16;            // elements of V a lane holds per key
-  constexpr int VP = (NE * ES + 15) / 16; // 16-byte pieces of them (8 bytes where NE * ES is 8)
   constexpr int VD = NE * ES / 4;         // dwords of them
   constexpr int ROWS = RW * RT * 16;      // query rows of a workgroup
   constexpr int LROW = DHP + 4;           // floats of an LDS row of O
+  // LDS of the keys: per stage and key wave 32 rows of K, then of V
+  constexpr int P = DHP * ES / 16;        // 16-byte pieces of a row
+  constexpr int TILE_BYTES = 2 * kTile * P * 16;
+  constexpr int ST = SHARED ? attn_stages(KW * TILE_BYTES) : 1;
+  constexpr int PASS = (kTile * P + RW * kWave - 1) / (RW * kWave);  // wave-loads of K (of V) that a wave makes at most
+  constexpr int PASS_LEAST = kTile * P / (RW * kWave);               // and at least
+  constexpr int KEY_BYTES = SHARED ? ST * KW * TILE_BYTES : 0;
+  constexpr int O_BYTES = KW > 1 ? NW * RT * 16 * LROW * 4 : 0;
 
-  __shared__ long long s_pre[kMaxAttnRows + 1], s_scan[kWaves];
-  __shared__ uint32_t s_anc[2][kMaxNodes][kMaxNodes / 32];
-  __shared__ int s_ptr[kMaxNodes], s_red[kWaves], s_last, s_odd;
-  __shared__ float s_ml[kWaves][RT * 16][2];
-  __shared__ __align__(16) float s_o[kWaves][16][LROW];
+  __shared__ int s_page[SHARED && PAGED ? kWindow : 1];
+  __shared__ __align__(1024) char s_mem[KEY_BYTES > O_BYTES ? KEY_BYTES : O_BYTES > 0 ? O_BYTES : 16];
+  __shared__ uint32_t s_anc[kMaxNodes][kMaxNodes / 32];
+  __shared__ int s_ptr[kMaxNodes], s_last, s_odd, s_hole;
+  __shared__ float s_ml[NW][RT * 16][2];
 
   const int t = threadIdx.x, lane = t & (kWave - 1), wave = uniform(t / kWave);
   const int c = lane & 15, g = lane >> 4;
   const int kw = wave % KW, rw = wave / KW;
   const int N = p.N, G = p.G, H = p.H, Dh = PAD ? p.Dh : DHP, M = N * G;
   const int tree_tiles = (N + kTile - 1) / kTile;
-  const int RB = (M + ROWS - 1) / ROWS;
+  const int RB = p.blocks, HR = H * RB;
   const size_t row_bytes = (size_t)Dh * ES;
 
-  // lengths of every row: the split of the work, and whether there is any
-  auto row_of = [&](int b) { return p.rows ? p.rows[b] : b; };
-  auto start_of = [&](int b, int len) { return p.width ? p.width[p.group > 0 ? b / p.group : 0] - len : 0; };
-  int bad = 0;
-  for (int b = t; b < p.B; b += kThreads) {
-    const int r = row_of(b);
-    if (r < 0 || r >= p.n_rows) {
-      bad = 1;
-    } else {
-      const int len = p.len[r], s = start_of(b, len);
-      bad |= len < 0 || s < 0 || (long long)s + len > p.cap;
+  // The split of the work (see plan).  Every wave finds it from the lengths.
+  Chunk k;
+  if (!plan<KW>(p, HR, tree_tiles, k)) return;
+  const int b = k.b, h = k.seg / RB, rb = k.seg - h * RB, r = k.row, len = k.len, start = k.start;
+  const int cache_tiles = (len + kTile - 1) / kTile, tiles = cache_tiles + tree_tiles;
+  const int t0 = k.unit0 * KW, t1 = min(tiles, k.unit1 * KW);
+
+  // the tree's parents come with the first loads
+  const bool need_anc = t1 > cache_tiles;
+  int raw_parent = 0;
+  if (need_anc && t < N) raw_parent = p.parent[(size_t)b * N + t];
+  if (t == 0) s_odd = s_hole = 0;
+  bool bad_page = false;
+
+  // Key i of tile tl: the page id to look up, and its row index (in units of Dh
+  // elements) from that.  Past the last key the last one is read again.  A bad
+  // page's keys take no part: the read stays inside the cache.
+  const uint32_t old0 = (uint32_t)((r * H + h) * p.cap + start), new0 = (uint32_t)((b * H + h) * N);
+  const int *table = PAGED ? p.table + (size_t)r * p.max_blocks : nullptr;
+  auto page_of = [&](int tl, int i) -> int {
+    if constexpr (!PAGED) return 0;
+    else return table[fdiv((uint32_t)max(min(tl * kTile + i, len - 1), 0), p.page_div)];
+  };
+  auto row_of = [&](int tl, int i, int page, bool &in) -> uint32_t {
+    if (tl >= cache_tiles) return new0 + (uint32_t)min((tl - cache_tiles) * kTile + i, N - 1);
+    const uint32_t pos = (uint32_t)min(tl * kTile + i, len - 1);
+    if constexpr (!PAGED) return old0 + pos;
+    else {
+      in = (uint32_t)page < (uint32_t)p.n_pages;
+      return ((in ? (uint32_t)page : 0u) * H + h) * p.page + (pos - fdiv(pos, p.page_div) * p.page);
     }
-  }
-  if (block_or_int<kThreads>(bad, s_red)) {
-    if (t == 0) set_status(p.status, SPECDEC_S_LEN_RANGE);
-    return;
-  }
-  block_prefix(p.B, s_pre, s_scan, [&](int b) {
-    const long long tiles = (p.len[row_of(b)] + kTile - 1) / kTile + tree_tiles;
-    return (tiles + KW - 1) / KW;
-  });
-  const long long HR = (long long)H * RB, total = s_pre[p.B] * HR;
-  const int W = (int)min((long long)gridDim.x, total);
-  // consecutive runs of work on one XCD (workgroups go to the 8 XCDs in turn),
-  // so query blocks that share keys share an L2
-  const int per_xcd = (W + 7) / 8, on_xcd = (int)(blockIdx.x >> 3);
-  const int w = (int)(blockIdx.x & 7) * per_xcd + on_xcd;
-  if (on_xcd >= per_xcd || w >= W) return;
-  const long long begin = total * w / W, end = total * (w + 1) / W;
+  };
 
-  const __amdgpu_buffer_rsrc_t wsr = coherent_rsrc(p.partial, p.partial_bytes);
-  constexpr int kSlotFloats = ROWS * (DHP + 4);  // per row: O, then max and sum (16-byte rows)
-  int anc_of = -1;
-
-  for (long long at = begin; at < end;) {
-    // the segment at `at`: batch row b, head h, query block rb
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (s_pre[mid] * HR <= at) lo = mid;
-      else hi = mid;
-    }
-    const int b = uniform(lo);
-    const long long units = s_pre[b + 1] - s_pre[b], rem = at - s_pre[b] * HR;
-    const int seg = uniform((int)(rem / units));
-    const long long u0 = rem - seg * units, seg0 = at - u0, seg1 = seg0 + units;
-    const long long u1 = min(units, u0 + (end - at));
-    at += u1 - u0;
-    const int h = seg / RB, rb = seg - h * RB;
-    const int r = uniform(row_of(b)), len = uniform(p.len[r]), start = uniform(start_of(b, len));
-    const int cache_tiles = (len + kTile - 1) / kTile, tiles = cache_tiles + tree_tiles;
-    const int t0 = (int)(u0 * KW), t1 = (int)min((long long)tiles, u1 * KW);
-
-    // which nodes each node attends: a bit per ancestor, by pointer doubling
-    if (t1 > cache_tiles && anc_of != b) {
-      __syncthreads();  // the last segment's readers
-      const int words = (N + 31) / 32;
-      bool bad_tree = false;
-      if (t < N) {
-        s_ptr[t] = node_parent(t, p.parent[(size_t)b * N + t], bad_tree);
-        for (int k = 0; k < words; ++k) s_anc[0][t][k] = (t >> 5) == k ? 1u << (t & 31) : 0u;
-      }
-      if (bad_tree) set_status(p.status, SPECDEC_S_TREE);
-      int side = 0;
-      for (int span = 1; span < N; span <<= 1, side ^= 1) {
-        __syncthreads();
-        int q = 0;
-        if (t < N) {
-          q = s_ptr[t];
-          for (int k = 0; k < words; ++k) s_anc[side ^ 1][t][k] = s_anc[side][t][k] | (q > 0 ? s_anc[side][q][k] : 0u);
-          if (q > 0) q = s_ptr[q];
-        }
-        __syncthreads();
-        if (t < N) s_ptr[t] = q;
-      }
-      __syncthreads();
-      // a node that reached the root sees it; one that did not sees nothing
-      if (t < N) {
-        for (int k = 0; k < words; ++k) {
-          const uint32_t m = s_anc[side][t][k];
-          s_anc[side ^ 1][t][k] = s_ptr[t] < 0 ? 0u : k == 0 ? m | 1u : m;
-        }
-      }
-      side ^= 1;
-      __syncthreads();
-      if (t < N && side)
-        for (int k = 0; k < words; ++k) s_anc[0][t][k] = s_anc[1][t][k];
-      __syncthreads();
-      anc_of = b;
-    }
-
-    // queries of this wave: row rt * 16 + c of its block, 16 bytes per step
-    const int rbase = rb * ROWS + rw * RT * 16;
-    u32x4 q[RT][KS];
-    int node[RT];
+  // queries of this wave: row rt * 16 + c of its block, 16 bytes per step
+  u32x4 q[RT][KS];
+  const int rbase = rb * ROWS + rw * RT * 16;
+  auto load_q = [&] {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int row = rbase + rt * 16 + c;
       const int n = row < M ? (int)fdiv((uint32_t)row, p.g_div) : 0, gq = row - n * G;
-      node[rt] = row < M ? n : -1;
       const char *src = static_cast<const char *>(p.q) +
                         ((int64_t)b * p.qs[0] + (int64_t)n * p.qs[1] + (int64_t)(h * G + gq) * p.qs[2]) * ES;
 #pragma unroll
@@ -339,315 +496,594 @@ __global__ __launch_bounds__(kThreads, attn_wgs_per_cu(RT, DHP)) void k_tree_att
         q[rt][s] = row < M && (!PAD || dh < Dh) ? *reinterpret_cast<const u32x4 *>(src + dh * ES) : (u32x4)(0u);
       }
     }
+  };
 
-    f32x4 o[RT][NE];
-    float m[RT], l[RT];
+  f32x4 o[RT][NE];
+  float m[RT];
+  f32x4 l[RT];  // every element the sum of the query's weights (fp32: of this lane's)
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    m[rt] = kLow;
+    l[rt] = (f32x4)(0.0f);
+#pragma unroll
+    for (int e = 0; e < NE; ++e) o[rt][e] = (f32x4)(0.0f);
+  }
+
+  // A tile's keys as the products take them: K of key kt * 16 + c, piece s * 4 +
+  // g; V of keys kt * 16 + g * 4 + 0 .. 3, NE elements from c * NE.
+  struct Keys {
+    u32x4 k[2][KS];
+    uint32_t v[8][VD];
+  };
+  auto split_v = [](uint32_t *v, const char *src, bool in, auto piece_in) {
+    if constexpr (VD == 2) {
+      const u32x2 w = in ? *reinterpret_cast<const u32x2 *>(src) : (u32x2)(0u);
+      v[0] = w[0];
+      v[1] = w[1];
+    } else {
+#pragma unroll
+      for (int d = 0; d < VD / 4; ++d) {
+        const u32x4 w = piece_in(d) ? *reinterpret_cast<const u32x4 *>(src + d * 16) : (u32x4)(0u);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) v[d * 4 + y] = w[y];
+      }
+    }
+  };
+  auto load_k = [&](Keys &x, int tl, uint32_t rho) {
+    const char *kb = static_cast<const char *>(tl < cache_tiles ? p.k_old : p.k_new);
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      const char *src = kb + (size_t)__shfl(rho, kt * 16 + c) * row_bytes + g * 16;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        x.k[kt][s] = !PAD || (s * 4 + g) * EL < Dh ? *reinterpret_cast<const u32x4 *>(src + s * 64) : (u32x4)(0u);
+    }
+  };
+  auto load_v = [&](Keys &x, int tl, uint32_t rho) {
+    const char *vb = static_cast<const char *>(tl < cache_tiles ? p.v_old : p.v_new);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      split_v(x.v[i], vb + (size_t)__shfl(rho, (i >> 2) * 16 + g * 4 + (i & 3)) * row_bytes + c * NE * ES,
+              !PAD || c * NE < Dh, [&](int d) { return !PAD || c * NE + d * EL < Dh; });
+  };
+  // The parts of a tile's work.  s[rt][kt][y] is of query c and key kt * 16 + g * 4
+  // + y: scores, then weights.
+  using Scores = f32x4[RT][2];
+  auto scores = [&](const Keys &x, Scores &s) {
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        s[rt][kt] = (f32x4)(0.0f);
+#pragma unroll
+        for (int y = 0; y < KS; ++y) s[rt][kt] = mma<DT>(x.k[kt][y], q[rt][y], s[rt][kt]);
+      }
+  };
+  // Keys that exist (vm) and, in the tree, that are part of it: what other nodes
+  // hold must not meet a zero weight as NaN.
+  auto existing = [&](int tl, uint32_t vm) -> uint32_t {
+    if (tl < cache_tiles) return vm;
+    const int j = (tl - cache_tiles) * kTile + (lane & (kTile - 1));
+    return vm & (uint32_t)__ballot(j < N && (s_anc[min(j, N - 1)][0] & 1u));
+  };
+  auto mask_scores = [&](Scores &s, int tl, uint32_t vm) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      m[rt] = kLow;
-      l[rt] = 0.0f;
+      uint32_t see = vm;
+      if (tl >= cache_tiles) {
+        const int row = rbase + rt * 16 + c;
+        see = row < M ? s_anc[fdiv((uint32_t)row, p.g_div)][tl - cache_tiles] : 0u;
+      }
+      see >>= g * 4;
 #pragma unroll
-      for (int e = 0; e < NE; ++e) o[rt][e] = (f32x4)(0.0f);
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) s[rt][kt][y] = see & (1u << (kt * 16 + y)) ? s[rt][kt][y] : -INFINITY;
     }
+  };
+  auto mask_values = [&](Keys &x, int tl, uint32_t vm) {
+    const uint32_t there = existing(tl, vm) >> (g * 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t on = there & (1u << ((i >> 2) * 16 + (i & 3))) ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+      for (int d = 0; d < VD; ++d) x.v[i][d] &= on;
+    }
+    // In the tree a node's V may only reach its descendants, but zero times
+    // infinity is NaN: where a tile holds a value that is not finite, zero takes
+    // its place here and the rows that attend to it add it at the end.
+    if (tl >= cache_tiles) {
+      uint32_t odd = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int d = 0; d < VD; ++d) odd |= odd_bits<DT>(x.v[i][d]);
+      if (__any(odd & (DT == 0 ? 0x80000000u : 0x80008000u))) {
+        s_odd = 1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int d = 0; d < VD; ++d) x.v[i][d] = finite_only<DT>(x.v[i][d]);
+      }
+    }
+  };
+  auto raise = [&](const Scores &s) {
+    float top[RT];
+    bool up = false;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      top[rt] = fmaxf(fmaxf(fmaxf(s[rt][0][0], s[rt][0][1]), fmaxf(s[rt][0][2], s[rt][0][3])),
+                      fmaxf(fmaxf(s[rt][1][0], s[rt][1][1]), fmaxf(s[rt][1][2], s[rt][1][3]))) * p.scale;
+      up |= top[rt] > m[rt] + kSlack;
+    }
+    if (!__any(up)) return;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      top[rt] = fmaxf(top[rt], __shfl_xor(top[rt], 16));
+      top[rt] = fmaxf(top[rt], __shfl_xor(top[rt], 32));
+      const float to = fmaxf(m[rt], top[rt]), f = __builtin_amdgcn_exp2f(m[rt] - to);
+      m[rt] = to;
+      l[rt] *= f;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) o[rt][e] *= f;
+    }
+  };
+  auto weights = [&](Scores &s, u32x4 (&w)[RT]) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) s[rt][kt][y] = __builtin_amdgcn_exp2f(fmaf(s[rt][kt][y], p.scale, -m[rt]));
+      if constexpr (DT == 0) {
+        l[rt][0] += ((s[rt][0][0] + s[rt][0][1]) + (s[rt][0][2] + s[rt][0][3])) +
+                    ((s[rt][1][0] + s[rt][1][1]) + (s[rt][1][2] + s[rt][1][3]));
+      } else {
+        w[rt] = u32x4{pack2<DT>(s[rt][0][0], s[rt][0][1]), pack2<DT>(s[rt][0][2], s[rt][0][3]),
+                      pack2<DT>(s[rt][1][0], s[rt][1][1]), pack2<DT>(s[rt][1][2], s[rt][1][3])};
+        // the sum of the rounded weights, by a product with ones: their roundings
+        // then mostly cancel in the quotient
+        constexpr uint32_t kOnes = DT == 1 ? 0x3C003C00u : 0x3F803F80u;
+        l[rt] = mma<DT>((u32x4)(kOnes), w[rt], l[rt]);
+      }
+    }
+  };
+  // O^T += V^T P^T
+  auto products = [&](const Keys &x, const Scores &s, const u32x4 (&w)[RT]) {
+    if constexpr (DT == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            o[rt][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x.v[i][e]), s[rt][i >> 2][i & 3], o[rt][e], 0,
+                                                            0, 0);
+    } else {
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
+        u32x4 a;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = __builtin_amdgcn_perm(x.v[2 * i + 1][e / 2], x.v[2 * i][e / 2], sel);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) o[rt][e] = mma<DT>(a, w[rt], o[rt][e]);
+      }
+    }
+  };
+  const int whole_tiles = min(t1, len / kTile);
 
-    if (t == 0) s_odd = 0;
-    __syncthreads();
-    bool bad_page = false;
-
-    // Row index (in units of Dh elements) of key lane & 31 of tile tl, and
-    // whether there is such a key.  A tile of the cache holds at least one.
+  if constexpr (!SHARED) {
+    // Keys straight into registers.  While a tile is multiplied the next is on its
+    // way, in registers of its own (NEXT) or in the same ones as they fall free.
+    // Page ids are looked up one tile further ahead, before the loads that need
+    // not wait for them (loads return in order).
     auto find = [&](int tl, bool &valid) -> uint32_t {
-      const int k = lane & (kTile - 1);
-      if (tl < cache_tiles) {
-        const int pos = tl * kTile + k;
-        valid = pos < len;
-        const int at_pos = valid ? pos : len - 1;
-        if (!p.table) return (uint32_t)((r * H + h) * p.cap + start + at_pos);
-        const int blk = (int)fdiv((uint32_t)at_pos, p.page_div), slot = at_pos - blk * p.page;
-        int pg = p.table[(size_t)r * p.max_blocks + blk];
-        if (pg < 0 || pg >= p.n_pages) {  // takes no part; the read stays inside the cache
-          pg = 0;
-          valid = false;
-          bad_page = true;
-        }
-        return (uint32_t)((pg * H + h) * p.page + slot);
-      }
-      const int j = (tl - cache_tiles) * kTile + k;
-      valid = j < N && tl < tiles && (s_anc[0][min(j, N - 1)][0] & 1u);
-      return (uint32_t)((b * H + h) * N + min(j, N - 1));
+      const int i = lane & (kTile - 1);
+      bool in = true;
+      const uint32_t rho = row_of(tl, i, page_of(tl, i), in);
+      bad_page |= !in;
+      valid = in && (tl < cache_tiles ? tl * kTile + i < len : (tl - cache_tiles) * kTile + i < N);
+      return rho;
     };
-    u32x4 kr[2][KS];
-    uint32_t vr[8][VD];
-    auto load_k = [&](int tl, uint32_t rho) {
-      const char *base = static_cast<const char *>(tl < cache_tiles ? p.k_old : p.k_new);
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-        const char *src = base + (size_t)__shfl(rho, kt * 16 + c) * row_bytes;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const int dh = (s * 4 + g) * EL;
-          kr[kt][s] = !PAD || dh < Dh ? *reinterpret_cast<const u32x4 *>(src + dh * ES) : (u32x4)(0u);
-        }
-      }
-    };
-    auto load_v = [&](int tl, uint32_t rho) {
-      const char *base = static_cast<const char *>(tl < cache_tiles ? p.v_old : p.v_new);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const char *src = base + (size_t)__shfl(rho, (k >> 2) * 16 + g * 4 + (k & 3)) * row_bytes + c * NE * ES;
-        if constexpr (VD == 2) {
-          const u32x2 v = !PAD || c * NE < Dh ? *reinterpret_cast<const u32x2 *>(src) : (u32x2)(0u);
-          vr[k][0] = v[0];
-          vr[k][1] = v[1];
-        } else {
-#pragma unroll
-          for (int d = 0; d < VP; ++d) {
-            const u32x4 v = !PAD || c * NE + d * EL < Dh ? *reinterpret_cast<const u32x4 *>(src + d * 16) : (u32x4)(0u);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) vr[k][d * 4 + x] = v[x];
-          }
-        }
-      }
-    };
-
+    Keys x0, x1;
     bool valid = false, valid_next = false;
     uint32_t rho = 0, rho_next = 0;
     int tl = t0 + kw;
     if (tl < t1) {
       rho = find(tl, valid);
-      load_k(tl, rho);
-      load_v(tl, rho);
       if (tl + KW < t1) rho_next = find(tl + KW, valid_next);
+      load_q();
+      load_k(x0, tl, rho);
+      load_v(x0, tl, rho);
     }
-    for (; tl < t1; tl += KW) {
+    if (need_anc) tree_ancestors(N, raw_parent, p.status, s_ptr, s_anc);
+    settle<DT>(q, p.negate);
+    uint32_t vm = (uint32_t)__ballot(valid);  // keys of the tile that exist
+    auto step = [&](auto plain) {
+      const uint32_t vm_now = vm, at_next = rho_next;
       const bool more = tl + KW < t1;
-      const uint32_t vm = (uint32_t)__ballot(valid);  // keys of the tile that exist
-      const bool in_tree = tl >= cache_tiles;
-      // scores: s[rt][kt][x] of query c and key kt * 16 + g * 4 + x
-      f32x4 s[RT][2];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          s[rt][kt] = (f32x4)(0.0f);
-#pragma unroll
-          for (int x = 0; x < KS; ++x) s[rt][kt] = mma<DT>(kr[kt][x], q[rt][x], s[rt][kt]);
-        }
-      if (more) load_k(tl + KW, rho_next);
-      const uint32_t mine = g * 4;
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) s[rt][kt] *= p.scale;  // log2(e) / sqrt(Dh), or the caller's
-        if (in_tree || vm != 0xFFFFFFFFu) {
-          uint32_t see = vm;
-          if (in_tree) see = node[rt] >= 0 ? s_anc[0][node[rt]][tl - cache_tiles] : 0u;
-#pragma unroll
-          for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (!((see >> (kt * 16 + mine + x)) & 1u)) s[rt][kt][x] = -INFINITY;
-        }
-        float top = fmaxf(fmaxf(fmaxf(s[rt][0][0], s[rt][0][1]), fmaxf(s[rt][0][2], s[rt][0][3])),
-                          fmaxf(fmaxf(s[rt][1][0], s[rt][1][1]), fmaxf(s[rt][1][2], s[rt][1][3])));
-        if (__any(top > m[rt] + kSlack)) {
-          top = fmaxf(top, __shfl_xor(top, 16));
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const float up = fmaxf(m[rt], top), f = __builtin_amdgcn_exp2f(m[rt] - up);
-          m[rt] = up;
-          l[rt] *= f;
-#pragma unroll
-          for (int e = 0; e < NE; ++e) o[rt][e] *= f;
-        }
-        float sum = 0.0f;
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            s[rt][kt][x] = __builtin_amdgcn_exp2f(s[rt][kt][x] - m[rt]);
-            sum += s[rt][kt][x];
-          }
-        l[rt] += sum;
-      }
-
-      // V of keys that do not exist must not meet their zero weights as NaN
-      if (vm != 0xFFFFFFFFu) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const bool on = (vm >> ((k >> 2) * 16 + mine + (k & 3))) & 1u;
-#pragma unroll
-          for (int d = 0; d < VD; ++d) vr[k][d] = on ? vr[k][d] : 0u;
+      vm = (uint32_t)__ballot(valid_next);
+      if (tl + 2 * KW < t1) rho_next = find(tl + 2 * KW, valid_next);
+      if constexpr (NEXT) {
+        if (more) {
+          load_k(x1, tl + KW, at_next);
+          load_v(x1, tl + KW, at_next);
         }
       }
-      // In the tree a node's V may only reach its descendants, but zero times
-      // infinity is NaN: where a tile holds a value that is not finite, zero takes
-      // its place here and the rows that attend to it add it at the segment's end.
-      if (in_tree) {
-        uint32_t odd = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-          for (int d = 0; d < VD; ++d) odd |= odd_bits<DT>(vr[k][d]);
-        if (__any(odd & (DT == 0 ? 0x80000000u : 0x80008000u))) {
-          s_odd = 1;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-#pragma unroll
-            for (int d = 0; d < VD; ++d) vr[k][d] = finite_only<DT>(vr[k][d]);
-        }
+      Scores s;
+      u32x4 w[RT];
+      scores(x0, s);
+      if constexpr (!NEXT) {
+        if (more) load_k(x0, tl + KW, at_next);
       }
-
-      // O^T += V^T P^T
-      if constexpr (DT == 0) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-          for (int e = 0; e < NE; ++e)
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-              o[rt][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vr[k][e]), s[rt][k >> 2][k & 3], o[rt][e], 0,
-                                                              0, 0);
+      if constexpr (!decltype(plain)::value) {
+        mask_scores(s, tl, vm_now);
+        mask_values(x0, tl, vm_now);
+      }
+      raise(s);
+      weights(s, w);
+      products(x0, s, w);
+      if constexpr (NEXT) {
+        x0 = x1;
       } else {
-        u32x4 w8[RT];
+        if (more) load_v(x0, tl + KW, at_next);
+      }
+      tl += KW;
+    };
+    while (tl < whole_tiles && vm == 0xFFFFFFFFu) step(std::true_type{});
+    while (tl < t1) step(std::false_type{});
+  } else {
+    // Keys through LDS, each piece loaded once for the RW waves that share it, by
+    // loads that write LDS directly: ST - 1 tiles are on their way while one is
+    // multiplied, and none of them holds a register.  A wave-load fills 64 slots of
+    // 16 bytes in a row; which piece of its row a slot holds is turned by swz(row),
+    // so that the 16 rows that one read of K touches lie in different banks.  All
+    // waves of the workgroup step together: a step waits for this wave's share of
+    // its tile, then for the others', starts the tile ST - 1 ahead (whose place the
+    // last step has freed) and multiplies.
+    const int in_group = rw * kWave + lane;
+    auto tile_of = [&](int i) { return t0 + kw + i * KW; };
+    const int mine = tile_of(0) < t1 ? (t1 - tile_of(0) + KW - 1) / KW : 0;  // tiles of this key wave
+    const int steps = (t1 - t0 + KW - 1) / KW;
+    // The page ids of the next kWindow blocks are kept in LDS: looked up tile by
+    // tile they would return in order with the keys that are on their way.
+    int window = 0;  // first block of it
+    auto fill_window = [&](int tl) {
+      window = (int)fdiv((uint32_t)min(tl * kTile, max(len - 1, 0)), p.page_div);
+      const int n = min(kWindow, (len + p.page - 1) / p.page - window);
+      for (int i = t; i < n; i += NT) {
+        const int page = table[window + i];
+        const bool in = (uint32_t)page < (uint32_t)p.n_pages;
+        if (!in) {
+          bad_page = true;
+          lds_set(lds_offset(&s_hole), 1u);
+        }
+        lds_set(lds_offset(&s_page[i]), in ? (uint32_t)page : 0u);
+      }
+    };
+    // the last tile whose blocks are all in it
+    auto window_end = [&] {
+      return (int)min((long long)(window + kWindow) * p.page / kTile - 1, (long long)cache_tiles - 1);
+    };
+    auto fetch = [&](int i) {
+      const int tl = tile_of(i);
+      const char *kb = static_cast<const char *>(tl < cache_tiles ? p.k_old : p.k_new);
+      const char *vb = static_cast<const char *>(tl < cache_tiles ? p.v_old : p.v_new);
+      char *to = s_mem + ((i % ST) * KW + kw) * TILE_BYTES + rw * (kWave * 16);
+#pragma unroll
+      for (int j = 0; j < PASS; ++j) {
+        const int row = (in_group + j * RW * kWave) / P;
+        if (kTile * P % (RW * kWave) != 0 && row >= kTile) break;  // whole waves, where RW is 3 or 6
+        const int piece = (in_group + j * RW * kWave) % P ^ swz<P>(row);
+        uint32_t rho;
+        if (tl >= cache_tiles) {
+          rho = new0 + (uint32_t)min((tl - cache_tiles) * kTile + row, N - 1);
+        } else {
+          const uint32_t pos = (uint32_t)min(tl * kTile + row, len - 1);
+          if constexpr (PAGED) {
+            const uint32_t blk = fdiv(pos, p.page_div);
+            rho = (lds_get(lds_offset(s_page) + (blk - (uint32_t)window) * 4u) * H + h) * p.page + (pos - blk * p.page);
+          } else {
+            rho = old0 + pos;
+          }
+        }
+        const size_t src = (size_t)rho * row_bytes + piece * 16;
+        if (!PAD || piece * EL < Dh) {
+          load_lds(kb + src, to + j * RW * kWave * 16);
+          load_lds(vb + src, to + j * RW * kWave * 16 + kTile * P * 16);
+        }
+      }
+    };
+    // Where this lane's pieces lie: K of row c, piece g of step 0 (step s: bits of
+    // 64 s turned), V of row g * 4 and its first piece (row g * 4 + i: bits of 16 i
+    // turned, i rows on; piece d likewise).  Tiles start at multiples of 1 KiB.
+    constexpr int HALF = 16 * P * 16;  // bytes from a tile's first 16 rows to its others
+    const uint32_t k_at = (uint32_t)(c * P * 16 + ((g ^ swz<P>(c)) << 4));
+    const uint32_t v_at = (uint32_t)((kTile + g * 4) * P * 16 + (((c * NE * ES >> 4) ^ swz<P>(g * 4)) << 4) + c * NE * ES % 16);
+    auto read_k = [&](Keys &x, uint32_t tile) {
+      const uint32_t a = tile + k_at;
+      if constexpr (KS == 2) {
+        lds_read<HALF>(x.k[0][0], x.k[0][1], x.k[1][0], x.k[1][1], a, a ^ 64u);
+      } else {
+#pragma unroll
+        for (int s = 0; s < KS; s += 4)
+          lds_read<HALF, 0, 0>(x.k[0][s], x.k[0][s + 1], x.k[0][s + 2], x.k[0][s + 3], x.k[1][s], x.k[1][s + 1],
+                               x.k[1][s + 2], x.k[1][s + 3], a ^ (64u * s), a ^ (64u * (s + 1)), a ^ (64u * (s + 2)),
+                               a ^ (64u * (s + 3)));
+      }
+    };
+    auto read_v = [&](Keys &x, uint32_t tile) {
+      const uint32_t a = tile + v_at;
+      // row g * 4 + i: its turn is (g * 4 + i) & 15, or of two rows of 8 pieces (g * 2 + i / 2) & 7
+      constexpr uint32_t T1 = P == 8 ? 0u : 16u, T2 = P == 8 ? 16u : 32u, T3 = P == 8 ? 16u : 48u;
+      constexpr int N_D = VD < 4 ? 1 : VD / 4;
+#pragma unroll
+      for (int d = 0; d < N_D; ++d) {
+        const uint32_t e = a ^ (16u * d);
+        if constexpr (VD == 2) {
+          u32x2 y[8];
+          lds_read<HALF, P * 16, 0>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], e, e ^ T1, e ^ T2, e ^ T3);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x.v[i][0] = y[i][0];
+            x.v[i][1] = y[i][1];
+          }
+        } else {
+          u32x4 y[8];
+          lds_read<HALF, P * 16, 0>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], e, e ^ T1, e ^ T2, e ^ T3);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) x.v[i][d * 4 + z] = y[i][z];
+        }
+      }
+    };
+    const uint32_t lds0 = lds_offset(s_mem) + kw * TILE_BYTES, hole_at = lds_offset(&s_hole);
+    if constexpr (PAD) {  // pieces past Dh are never written: they read as zeros
+      for (int i = t; i < ST * KW * TILE_BYTES / 16; i += NT) reinterpret_cast<u32x4 *>(s_mem)[i] = (u32x4)(0u);
+    }
+    // the first window, wherever the part's first tiles lie
+    const bool has_old = PAGED && t0 < cache_tiles;
+    load_q();
+    __syncthreads();  // s_hole
+    if (has_old) fill_window(t0);
+    if (need_anc) tree_ancestors(N, raw_parent, p.status, s_ptr, s_anc);
+    else __syncthreads();  // the window, and the zeros
+    settle<DT>(q, p.negate);
+    int filled = has_old ? window_end() : 0x7FFFFFFF;
+    // every wave of the workgroup comes here: the window moves for all together
+    auto next_fetch = [&](int i) {
+      if (PAGED && t0 + i * KW + KW - 1 > filled && t0 + i * KW < cache_tiles) {
+        barrier();
+        fill_window(t0 + i * KW);
+        filled = window_end();
+        if (filled == cache_tiles - 1) filled = 0x7FFFFFFF;
+        barrier();
+      }
+      if (i < mine) fetch(i);
+    };
+    if (filled == cache_tiles - 1) filled = 0x7FFFFFFF;
+#pragma unroll
+    for (int i = 0; i + 1 < ST; ++i) next_fetch(i);
+    // keys of a tile that exist: all but the last ones, unless some page was bad
+    auto existing_keys = [&](int tl, bool hole) -> uint32_t {
+      const int n = tl < cache_tiles ? len - tl * kTile : N - (tl - cache_tiles) * kTile;
+      uint32_t vm = n >= kTile ? 0xFFFFFFFFu : (1u << n) - 1u;
+      if (hole && tl < cache_tiles) {
+        bool in = true;
+        row_of(tl, lane & (kTile - 1), page_of(tl, lane & (kTile - 1)), in);
+        vm &= (uint32_t)__ballot(in);
+      }
+      return vm;
+    };
+    Keys x;
+    Scores s;
+    u32x4 w[RT];
+    // A step multiplies V of tile i and, where three tiles fit LDS, already K of
+    // tile i + 1: its scores need nothing of the softmax that goes on meanwhile.
+    constexpr int AHEAD = ST > 2 ? 1 : 0;
+    auto new_scores = [&](int i, bool hole) {
+      const int tl = tile_of(i);
+      read_k(x, lds0 + (uint32_t)((i % ST) * KW * TILE_BYTES));
+      scores(x, s);
+      const uint32_t vm = existing_keys(tl, hole);
+      if (tl >= cache_tiles || vm != 0xFFFFFFFFu) mask_scores(s, tl, vm);
+    };
+    if constexpr (AHEAD == 1) {
+      if (ST - 2 < mine) wait_loads<2 * PASS_LEAST * (ST - 2)>();
+      else wait_loads<0>();
+      barrier();
+      if (mine > 0) {
+        new_scores(0, uniform((int)lds_get(hole_at)) != 0);
+        raise(s);
+      }
+    }
+    for (int i = 0; i < steps; ++i) {
+      // this wave's loads of tile i + AHEAD: those of the tiles after it may be out
+      if (i + ST - 2 < mine) wait_loads<2 * PASS_LEAST * (ST - 2 - AHEAD)>();
+      else wait_loads<0>();
+      barrier();
+      const bool hole = uniform((int)lds_get(hole_at)) != 0;
+      next_fetch(i + ST - 1);
+      const uint32_t tile = lds0 + (uint32_t)((i % ST) * KW * TILE_BYTES);
+      if (AHEAD == 1 && tile_of(i + 1) < whole_tiles && !hole) {
+        Scores next;
+        read_k(x, lds0 + (uint32_t)(((i + 1) % ST) * KW * TILE_BYTES));
+        scores(x, next);
+        weights(s, w);
+        __builtin_amdgcn_sched_barrier(0);  // K's registers are free before V's fill
+        read_v(x, tile);
+        products(x, s, w);
+        raise(next);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
-          w8[rt] = u32x4{pack2<DT>(s[rt][0][0], s[rt][0][1]), pack2<DT>(s[rt][0][2], s[rt][0][3]),
-                         pack2<DT>(s[rt][1][0], s[rt][1][1]), pack2<DT>(s[rt][1][2], s[rt][1][3])};
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-          const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
-          u32x4 a;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) a[k] = __builtin_amdgcn_perm(vr[2 * k + 1][e / 2], vr[2 * k][e / 2], sel);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) o[rt][e] = mma<DT>(a, w8[rt], o[rt][e]);
+          for (int kt = 0; kt < 2; ++kt) s[rt][kt] = next[rt][kt];
+      } else if (i < mine) {
+        const int tl = tile_of(i);
+        if constexpr (AHEAD == 0) {
+          new_scores(i, hole);
+          raise(s);
+        }
+        read_v(x, tile);
+        const uint32_t vm = existing_keys(tl, hole);
+        if (tl >= cache_tiles || vm != 0xFFFFFFFFu) mask_values(x, tl, vm);
+        weights(s, w);
+        products(x, s, w);
+        if (AHEAD == 1 && i + 1 < mine) {
+          new_scores(i + 1, hole);
+          raise(s);
         }
       }
-      if (more) {
-        load_v(tl + KW, rho_next);
-        rho = rho_next;
-        valid = valid_next;
-        if (tl + 2 * KW < t1) rho_next = find(tl + 2 * KW, valid_next);
-      }
     }
+    __syncthreads();  // the keys' LDS is free
+  }
+  if (bad_page) set_status(p.status, SPECDEC_S_LEN_RANGE);
 
-    if (bad_page) set_status(p.status, SPECDEC_S_LEN_RANGE);
-    // The segment's end: sums over lane groups, then over the key waves.
+  // The end: every query's maximum and sum over lane groups and key waves, then
+  // O over the key waves.
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    float sum = l[rt][0];
+    if constexpr (DT == 0) {
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+    }
+    if (g == 0) {
+      s_ml[wave][rt * 16 + c][0] = m[rt];
+      s_ml[wave][rt * 16 + c][1] = sum;
+    }
+  }
+  __syncthreads();
+  const __amdgpu_buffer_rsrc_t wsr = coherent_rsrc(p.partial, p.partial_bytes);
+  constexpr uint32_t kSlotBytes = ROWS * LROW * 4;  // per row: O, then max and sum (16-byte rows)
+  const uint32_t slot = (uint32_t)k.slot * kSlotBytes;
+  const bool odd = s_odd;
+  const char *nv = static_cast<const char *>(p.v_new) + (size_t)(b * H + h) * N * row_bytes;
+  // elements e .. e+7 of a block's row: to the output, or to the workspace
+  auto finish = [&](int brow, int e, f32x4 a, f32x4 d, float mx, float sum) {
+    const int row = rb * ROWS + brow;
+    if (row >= M || e >= Dh) return;
+    if (odd) add_odd<DT>(p, nv, row, e, Dh, t0 - cache_tiles, t1 - cache_tiles, s_anc, a, d);
+    if (k.slot < 0) {
+      store_out<DT>(p, b, h, row, e, a, d, 1.0f / sum, s_anc);
+    } else {
+      const uint32_t off = slot + (uint32_t)(brow * LROW) * 4u;
+      st_f4(wsr, off + (uint32_t)e * 4u, a);
+      st_f4(wsr, off + (uint32_t)e * 4u + 16u, d);
+      if (e == 0) st_f4(wsr, off + DHP * 4u, f32x4{mx, sum, 0.0f, 0.0f});
+    }
+  };
+  if constexpr (KW == 1) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      l[rt] += __shfl_xor(l[rt], 16);
-      l[rt] += __shfl_xor(l[rt], 32);
-      if (g == 0) {
-        s_ml[wave][rt * 16 + c][0] = m[rt];
-        s_ml[wave][rt * 16 + c][1] = l[rt];
-      }
+      const float mx = m[rt], sum = s_ml[wave][rt * 16 + c][1];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int e = 0; e < NE; e += NE < 8 ? NE : 8) {
+          if constexpr (NE >= 8) {
+            finish((rw * RT + rt) * 16 + c, (g * 4 + x) * NE + e,
+                   f32x4{o[rt][e][x], o[rt][e + 1][x], o[rt][e + 2][x], o[rt][e + 3][x]},
+                   f32x4{o[rt][e + 4][x], o[rt][e + 5][x], o[rt][e + 6][x], o[rt][e + 7][x]}, mx, sum);
+          } else if (x % 2 == 0) {  // Dh = 64: eight elements are two rows of the product
+            finish((rw * RT + rt) * 16 + c, (g * 4 + x) * NE,
+                   f32x4{o[rt][0][x], o[rt][1][x], o[rt][2][x], o[rt][3][x]},
+                   f32x4{o[rt][0][x + 1], o[rt][1][x + 1], o[rt][2][x + 1], o[rt][3][x + 1]}, mx, sum);
+          }
+        }
     }
-    __syncthreads();
-    const bool whole = u0 == 0 && u1 == units;
-    // this workgroup's slot: its run's first segment if that began earlier, its
-    // last if it goes on
-    const uint32_t slot = (uint32_t)(w * 2 + (u0 == 0)) * (uint32_t)(kSlotFloats * 4);
-    // 16-byte pieces of a tile's rows: thread -> (row, first element)
-    constexpr int PIECES = DHP / 8;  // of 8 elements
+  } else {
+    float(*s_o)[RT * 16][LROW] = reinterpret_cast<float(*)[RT * 16][LROW]>(s_mem);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       float top = kLow;
 #pragma unroll
-      for (int k = 0; k < KW; ++k) top = fmaxf(top, s_ml[rw * KW + k][rt * 16 + c][0]);
+      for (int i = 0; i < KW; ++i) top = fmaxf(top, s_ml[rw * KW + i][rt * 16 + c][0]);
       const float f = __builtin_amdgcn_exp2f(m[rt] - top);
-      if (rt) __syncthreads();
 #pragma unroll
       for (int x = 0; x < 4; ++x)
 #pragma unroll
         for (int e = 0; e < NE; e += 4)
-          *reinterpret_cast<f32x4 *>(&s_o[wave][c][(g * 4 + x) * NE + e]) =
+          *reinterpret_cast<f32x4 *>(&s_o[wave][rt * 16 + c][(g * 4 + x) * NE + e]) =
               f32x4{o[rt][e][x], o[rt][e + 1][x], o[rt][e + 2][x], o[rt][e + 3][x]} * f;
-      __syncthreads();
-      for (int i = t; i < RW * 16 * PIECES; i += kThreads) {
-        const int e = i % PIECES * 8, rr = i / PIECES, wq = rr / 16, rc = rr % 16;
-        const int brow = (wq * RT + rt) * 16 + rc, row = rb * ROWS + brow;
-        if (row >= M || e >= Dh) continue;
-        f32x4 a = (f32x4)(0.0f), d = (f32x4)(0.0f);
-        float mx = kLow, sum = 0.0f;
+    }
+    __syncthreads();
+    constexpr int PIECES = DHP / 8;  // of 8 elements: a thread's share of a row
+    const int most = min(ROWS, M - rb * ROWS);
+    for (int i = t; i < most * PIECES; i += NT) {
+      const int e = i % PIECES * 8, brow = i / PIECES, wq = brow / (RT * 16), rr = brow % (RT * 16);
+      f32x4 a = (f32x4)(0.0f), d = (f32x4)(0.0f);
+      float mx = kLow, sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KW; ++k) {
-          a += *reinterpret_cast<const f32x4 *>(&s_o[wq * KW + k][rc][e]);
-          d += *reinterpret_cast<const f32x4 *>(&s_o[wq * KW + k][rc][e + 4]);
-          mx = fmaxf(mx, s_ml[wq * KW + k][rt * 16 + rc][0]);
-        }
+      for (int j = 0; j < KW; ++j) {
+        a += *reinterpret_cast<const f32x4 *>(&s_o[wq * KW + j][rr][e]);
+        d += *reinterpret_cast<const f32x4 *>(&s_o[wq * KW + j][rr][e + 4]);
+        mx = fmaxf(mx, s_ml[wq * KW + j][rr][0]);
+      }
 #pragma unroll
-        for (int k = 0; k < KW; ++k)
-          sum += s_ml[wq * KW + k][rt * 16 + rc][1] * __builtin_amdgcn_exp2f(s_ml[wq * KW + k][rt * 16 + rc][0] - mx);
-        if (s_odd)
-          add_odd<DT>(p, static_cast<const char *>(p.v_new) + (size_t)(b * H + h) * N * row_bytes, row, e, Dh, t0 - cache_tiles,
-                      t1 - cache_tiles, s_anc[0], a, d);
-        if (whole) {
-          store_out<DT>(p, b, h, row, e, a, d, 1.0f / sum, s_anc[0]);
-        } else {
-          const uint32_t off = slot + (uint32_t)(brow * (DHP + 4)) * 4u;
-          st_f4(wsr, off + (uint32_t)e * 4u, a);
-          st_f4(wsr, off + (uint32_t)e * 4u + 16u, d);
-          if (e == 0) st_f4(wsr, off + DHP * 4u, f32x4{mx, sum, 0.0f, 0.0f});
-        }
+      for (int j = 0; j < KW; ++j)
+        sum += s_ml[wq * KW + j][rr][1] * __builtin_amdgcn_exp2f(s_ml[wq * KW + j][rr][0] - mx);
+      finish(brow, e, a, d, mx, sum);
+    }
+  }
+  if (k.slot < 0) return;
+
+  // One of several workgroups of the segment: the last to arrive adds them.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (t == 0) {
+    unsigned int *count = p.counters + (size_t)k.slot0 * kCountStride;
+    const bool last = atomicAdd(count, 1u) == (unsigned)(k.parts - 1);
+    if (last) store_agent(count, 0u);
+    s_last = last;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  if (!need_anc) tree_ancestors(N, t < N ? p.parent[(size_t)b * N + t] : 0, p.status, s_ptr, s_anc);
+  constexpr int PIECES = DHP / 8, NB = 4;  // parts whose loads are in flight together
+  const int most = min(ROWS, M - rb * ROWS);
+  for (int i = t; i < most * PIECES; i += NT) {
+    const int e = i % PIECES * 8, brow = i / PIECES;
+    if (e >= Dh) continue;
+    f32x4 a = (f32x4)(0.0f), d = (f32x4)(0.0f);
+    float mx = kLow, sum = 0.0f;
+    const uint32_t off = (uint32_t)k.slot0 * kSlotBytes + (uint32_t)(brow * LROW) * 4u;
+    for (int j0 = 0; j0 < k.parts; j0 += NB) {
+      f32x4 ml[NB], pa[NB], pd[NB];
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const uint32_t at = off + (uint32_t)min(j0 + j, k.parts - 1) * kSlotBytes;
+        ml[j] = ld_f4(wsr, at + DHP * 4u);
+        pa[j] = ld_f4(wsr, at + (uint32_t)e * 4u);
+        pd[j] = ld_f4(wsr, at + (uint32_t)e * 4u + 16u);
+      }
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        if (j0 + j >= k.parts) break;
+        const float up = fmaxf(mx, ml[j][0]), fo = __builtin_amdgcn_exp2f(mx - up), fn = __builtin_amdgcn_exp2f(ml[j][0] - up);
+        a = a * fo + pa[j] * fn;
+        d = d * fo + pd[j] * fn;
+        sum = sum * fo + ml[j][1] * fn;
+        mx = up;
       }
     }
-    if (!whole) {
-      // the segment's workgroups: the first holds its unit 0, the last its end
-      const int w0 = first_wg(seg0, total, W), w1 = first_wg(seg1 - 1, total, W);
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      if (t == 0) {
-        unsigned int *count = p.counters + (size_t)w0 * kCountStride;
-        const bool last = atomicAdd(count, 1u) == (unsigned)(w1 - w0);
-        if (last) store_agent(count, 0u);
-        s_last = last;
-      }
-      __syncthreads();
-      if (s_last) {
-        if (anc_of != b) {
-          // only whether a node is used matters here
-          __syncthreads();
-          bool bt = false;
-          if (t < N) s_ptr[t] = node_parent(t, p.parent[(size_t)b * N + t], bt);
-          for (int span = 1; span < N; span <<= 1) {
-            __syncthreads();
-            const int q1 = t < N && s_ptr[t] > 0 ? s_ptr[s_ptr[t]] : t < N ? s_ptr[t] : 0;
-            __syncthreads();
-            if (t < N) s_ptr[t] = q1;
-          }
-          if (t < N) s_anc[0][t][0] = s_ptr[t] == 0;
-          __syncthreads();
-          anc_of = -1;
-        }
-        for (int i = t; i < ROWS * PIECES; i += kThreads) {
-          const int e = i % PIECES * 8, brow = i / PIECES, row = rb * ROWS + brow;
-          if (row >= M || e >= Dh) continue;
-          f32x4 a = (f32x4)(0.0f), d = (f32x4)(0.0f);
-          float mx = kLow, sum = 0.0f;
-          for (int k = w0; k <= w1; ++k) {
-            const uint32_t off = (uint32_t)(k * 2 + (k == w0)) * (uint32_t)(kSlotFloats * 4) + (uint32_t)(brow * (DHP + 4)) * 4u;
-            const f32x4 ml = ld_f4(wsr, off + DHP * 4u);
-            const f32x4 ka = ld_f4(wsr, off + (uint32_t)e * 4u), kd = ld_f4(wsr, off + (uint32_t)e * 4u + 16u);
-            const float up = fmaxf(mx, ml[0]), fo = __builtin_amdgcn_exp2f(mx - up), fn = __builtin_amdgcn_exp2f(ml[0] - up);
-            a = a * fo + ka * fn;
-            d = d * fo + kd * fn;
-            sum = sum * fo + ml[1] * fn;
-            mx = up;
-          }
-          store_out<DT>(p, b, h, row, e, a, d, 1.0f / sum, s_anc[0]);
-        }
-      }
-    }
-    __syncthreads();  // s_ml, s_o and s_anc are free again
+    store_out<DT>(p, b, h, rb * ROWS + brow, e, a, d, 1.0f / sum, s_anc);
   }
 }
 
-template <int DT, int DHP, int RT, int RW>
+template <int DT, int DHP, int RT, int RW, int KW>
 static hipError_t launch_attn(const TreeAttnParams &p, hipStream_t s) {
-  if (p.Dh == DHP)
-    hipLaunchKernelGGL((k_tree_attention<DT, DHP, RT, RW, false>), dim3((unsigned)p.grid), dim3(kThreads), 0, s, p);
+  const dim3 grid((unsigned)p.grid), block(RW * KW * kWave);
+  if (p.table && p.Dh == DHP)
+    hipLaunchKernelGGL((k_tree_attention<DT, DHP, RT, RW, KW, true, false>), grid, block, 0, s, p);
+  else if (p.table)
+    hipLaunchKernelGGL((k_tree_attention<DT, DHP, RT, RW, KW, true, true>), grid, block, 0, s, p);
+  else if (p.Dh == DHP)
+    hipLaunchKernelGGL((k_tree_attention<DT, DHP, RT, RW, KW, false, false>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((k_tree_attention<DT, DHP, RT, RW, true>), dim3((unsigned)p.grid), dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_tree_attention<DT, DHP, RT, RW, KW, false, true>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
@@ -655,17 +1091,18 @@ static hipError_t launch_attn(const TreeAttnParams &p, hipStream_t s) {
 template <int DT, int DHP>
 static hipError_t launch_attn_dh(const TreeAttnParams &p, const AttnShape &a, hipStream_t s) {
   constexpr int kMost = attn_most_tiles(DT, DHP);
-  if (a.rw == 1) {
-    if (a.rt == 1) return launch_attn<DT, DHP, 1, 1>(p, s);
-    if constexpr (kMost >= 2)
-      if (a.rt == 2) return launch_attn<DT, DHP, 2, 1>(p, s);
-    if constexpr (kMost >= 4)
-      if (a.rt == 4) return launch_attn<DT, DHP, 4, 1>(p, s);
+  if (a.rw == 1 && a.rt == 1) return launch_attn<DT, DHP, 1, 1, 4>(p, s);
+  if constexpr (kMost == 2) {
+    if (a.rw == 1) return launch_attn<DT, DHP, 2, 1, 4>(p, s);
+    if (a.rt == 2) return launch_attn<DT, DHP, 2, 8, 1>(p, s);
+    if (a.rw == 6) return launch_attn<DT, DHP, 1, 6, 1>(p, s);
   }
-  if constexpr (kMost >= 4)
-    if (a.rt == 3 && a.rw == 2) return launch_attn<DT, DHP, 3, 2>(p, s);
-  if (a.rt == kMost && a.rw == 2) return launch_attn<DT, DHP, kMost, 2>(p, s);
-  if (a.rt == kMost && a.rw == 4) return launch_attn<DT, DHP, kMost, 4>(p, s);
+  if constexpr (attn_waves_per_simd(DT, DHP) == 2) {
+    if (a.rw == 4) return launch_attn<DT, DHP, 1, 4, 2>(p, s);
+    if (a.rw == 8) return launch_attn<DT, DHP, 1, 8, 1>(p, s);
+  } else {
+    if (a.rw == 4) return launch_attn<DT, DHP, 1, 4, 1>(p, s);
+  }
   return hipErrorInvalidValue;
 }
 

@@ -806,18 +806,17 @@ AttnShape attn_shape(int dtype, int Dh, int M) {
   AttnShape a;
   a.dhp = Dh <= 64 ? 64 : Dh <= 128 ? 128 : 256;
   const int most = attn_most_tiles(dtype, a.dhp);
-  if (M <= 16 * most) {
-    a.rt = M <= 16 ? 1 : 2;
+  if (M <= 16 * most || !attn_shared(dtype, a.dhp)) {
+    a.rt = M <= 16 || most == 1 ? 1 : 2;
     a.rw = 1;
     a.kw = 4;
     return a;
   }
-  const bool wide = attn_waves_per_simd(dtype, a.dhp) == 1;  // fp32 heads over 128
   a.kw = 1;
   a.rt = 1;
-  if (wide || M <= 64) {
+  if (M <= 64 && attn_share_keys(dtype, a.dhp) == 2) {
     a.rw = 4;
-    a.kw = wide ? 1 : 2;
+    a.kw = 2;
   } else if (most == 2 && (M <= 96 || (M > 128 && M <= 192))) {
     a.rw = 6;  // blocks of 96 rows: the least rows left over
   } else {
@@ -829,7 +828,7 @@ AttnShape attn_shape(int dtype, int Dh, int M) {
 
 // Workgroups that the device holds at once.
 int attn_resident(int dtype, const AttnShape &a) {
-  return device_cus() * (4 * attn_waves_per_simd(dtype, a.dhp) / (a.rw * a.kw) > 1 ? 2 : 1);
+  return device_cus() * (a.rw == 1 ? attn_direct_wgs(dtype, a.dhp) : 1);
 }
 }  // namespace sd
 

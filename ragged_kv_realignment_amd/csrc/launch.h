@@ -53,11 +53,16 @@ struct AttnShape {
   size_t part_bytes() const { return (size_t)rows() * (dhp + 4) * 4; }
 };
 
-// Waves per SIMD, and 16-row query tiles that a wave can hold beside its keys in
-// the registers that leaves (256, or 512 for fp32 heads over 128).
-constexpr int attn_waves_per_simd(int dtype, int dhp) { return dtype == 0 && dhp == 256 ? 1 : 2; }
-// Tiles in LDS of a stage's bytes: at most six, in 128 KiB.
-constexpr int attn_stages(int bytes) { return 131072 / bytes > 6 ? 6 : 131072 / bytes; }
+// Whether waves of an instance share keys through LDS (of which three tiles and
+// more have to fit), and the waves that take other keys beside four that share.
+constexpr bool attn_shared(int dtype, int dhp) { return !(dtype == 0 && dhp == 256); }
+constexpr int attn_share_keys(int dtype, int dhp) { return dhp * (dtype == 0 ? 2 : 1) <= 128 ? 2 : 1; }
+// Tiles in 128 KiB of LDS (per key wave), at most eight.
+constexpr int attn_stages(int bytes) { return 131072 / bytes >= 8 ? 8 : 131072 / bytes; }
+// Workgroups per CU of four waves that share none: two of 256 registers, or one
+// of 512 where two tiles of keys take more.
+constexpr int attn_direct_wgs(int dtype, int dhp) { return dhp * (dtype == 0 ? 2 : 1) <= 128 ? 2 : 1; }
+// 16-row query tiles that a wave holds at most.
 constexpr int attn_most_tiles(int dtype, int dhp) { return dhp * (dtype == 0 ? 2 : 1) <= 128 ? 2 : 1; }
 AttnShape attn_shape(int dtype, int Dh, int M);
 int attn_resident(int dtype, const AttnShape &a);  // workgroups that the device holds at once

@@ -60,7 +60,7 @@ namespace {
 constexpr int kTile = 32;        // keys of a wave's step
 constexpr float kSlack = 8.0f;   // log2 of the largest weight before the maximum is raised
 constexpr int kWindow = 1024;       // page ids in LDS
-constexpr uint32_t kMinUnits = 4; // of a part (see plan)
+constexpr int kMinUnits = 4;      // of a part (see plan)
 constexpr float kLow = -1e30f;   // running maximum before the first key
 
 template <int DT> constexpr int es() { return DT == 0 ? 4 : 2; }
@@ -85,13 +85,21 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
   if constexpr (DT == 1) {
-    const _Float16 a = (_Float16)lo, b = (_Float16)hi;
-    return (uint32_t)__builtin_bit_cast(uint16_t, a) | (uint32_t)__builtin_bit_cast(uint16_t, b) << 16;
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), f16x2));
   } else {
-    const __bf16 a = (__bf16)lo, b = (__bf16)hi;
-    return (uint32_t)__builtin_bit_cast(uint16_t, a) | (uint32_t)__builtin_bit_cast(uint16_t, b) << 16;
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
   }
+}
+
+// The largest of eight scores, NaN passed over.  (The median with +inf is the
+// larger of two; fmaxf would first canonicalise each operand.)
+__device__ __forceinline__ float max8(f32x4 a, f32x4 b) {
+  auto larger = [](float x, float y) { return __builtin_amdgcn_fmed3f(x, y, INFINITY); };
+  return larger(larger(larger(a[0], a[1]), larger(a[2], a[3])), larger(larger(b[0], b[1]), larger(b[2], b[3])));
 }
 
 template <int DT>
@@ -236,29 +244,44 @@ __device__ __forceinline__ void lds_read(u32x4 &a, u32x4 &b, u32x4 &c, u32x4 &d,
       : "v"(p), "v"(q), "n"(OFF)
       : "memory");
 }
-// The rows at q, r and s lie ROW, 2 ROW and 3 ROW bytes on.
-template <int OFF, int ROW, int>
+template <int OFF>
 __device__ __forceinline__ void lds_read(u32x4 &a, u32x4 &b, u32x4 &c, u32x4 &d, u32x4 &e, u32x4 &f, u32x4 &g, u32x4 &h,
                                          uint32_t p, uint32_t q, uint32_t r, uint32_t s) {
   asm volatile(
-      "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9 offset:%12\n\tds_read_b128 %2, %10 offset:%13\n\t"
-      "ds_read_b128 %3, %11 offset:%14\n\tds_read_b128 %4, %8 offset:%15\n\tds_read_b128 %5, %9 offset:%16\n\t"
-      "ds_read_b128 %6, %10 offset:%17\n\tds_read_b128 %7, %11 offset:%18\n\ts_waitcnt lgkmcnt(0)"
+      "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %10\n\tds_read_b128 %3, %11\n\t"
+      "ds_read_b128 %4, %8 offset:%12\n\tds_read_b128 %5, %9 offset:%12\n\tds_read_b128 %6, %10 offset:%12\n\t"
+      "ds_read_b128 %7, %11 offset:%12\n\ts_waitcnt lgkmcnt(0)"
       : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h)
-      : "v"(p), "v"(q), "v"(r), "v"(s), "n"(ROW), "n"(2 * ROW), "n"(3 * ROW), "n"(OFF), "n"(OFF + ROW), "n"(OFF + 2 * ROW),
-        "n"(OFF + 3 * ROW)
+      : "v"(p), "v"(q), "v"(r), "v"(s), "n"(OFF)
       : "memory");
 }
-template <int OFF, int ROW, int>
-__device__ __forceinline__ void lds_read(u32x2 &a, u32x2 &b, u32x2 &c, u32x2 &d, u32x2 &e, u32x2 &f, u32x2 &g, u32x2 &h,
-                                         uint32_t p, uint32_t q, uint32_t r, uint32_t s) {
+// The rows at q, r and s lie ROW, 2 ROW and 3 ROW bytes on; and two words.
+template <int OFF, int ROW>
+__device__ __forceinline__ void lds_read(u32x4 &a, u32x4 &b, u32x4 &c, u32x4 &d, u32x4 &e, u32x4 &f, u32x4 &g, u32x4 &h,
+                                         uint32_t &y, uint32_t &z, uint32_t p, uint32_t q, uint32_t r, uint32_t s,
+                                         uint32_t at_y, uint32_t at_z) {
   asm volatile(
-      "ds_read_b64 %0, %8\n\tds_read_b64 %1, %9 offset:%12\n\tds_read_b64 %2, %10 offset:%13\n\t"
-      "ds_read_b64 %3, %11 offset:%14\n\tds_read_b64 %4, %8 offset:%15\n\tds_read_b64 %5, %9 offset:%16\n\t"
-      "ds_read_b64 %6, %10 offset:%17\n\tds_read_b64 %7, %11 offset:%18\n\ts_waitcnt lgkmcnt(0)"
-      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h)
-      : "v"(p), "v"(q), "v"(r), "v"(s), "n"(ROW), "n"(2 * ROW), "n"(3 * ROW), "n"(OFF), "n"(OFF + ROW), "n"(OFF + 2 * ROW),
-        "n"(OFF + 3 * ROW)
+      "ds_read_b128 %0, %10\n\tds_read_b128 %1, %11 offset:%16\n\tds_read_b128 %2, %12 offset:%17\n\t"
+      "ds_read_b128 %3, %13 offset:%18\n\tds_read_b128 %4, %10 offset:%19\n\tds_read_b128 %5, %11 offset:%20\n\t"
+      "ds_read_b128 %6, %12 offset:%21\n\tds_read_b128 %7, %13 offset:%22\n\tds_read_b32 %8, %14\n\tds_read_b32 %9, %15\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h), "=&v"(y), "=&v"(z)
+      : "v"(p), "v"(q), "v"(r), "v"(s), "v"(at_y), "v"(at_z), "n"(ROW), "n"(2 * ROW), "n"(3 * ROW), "n"(OFF), "n"(OFF + ROW),
+        "n"(OFF + 2 * ROW), "n"(OFF + 3 * ROW)
+      : "memory");
+}
+template <int OFF, int ROW>
+__device__ __forceinline__ void lds_read(u32x2 &a, u32x2 &b, u32x2 &c, u32x2 &d, u32x2 &e, u32x2 &f, u32x2 &g, u32x2 &h,
+                                         uint32_t &y, uint32_t &z, uint32_t p, uint32_t q, uint32_t r, uint32_t s,
+                                         uint32_t at_y, uint32_t at_z) {
+  asm volatile(
+      "ds_read_b64 %0, %10\n\tds_read_b64 %1, %11 offset:%16\n\tds_read_b64 %2, %12 offset:%17\n\t"
+      "ds_read_b64 %3, %13 offset:%18\n\tds_read_b64 %4, %10 offset:%19\n\tds_read_b64 %5, %11 offset:%20\n\t"
+      "ds_read_b64 %6, %12 offset:%21\n\tds_read_b64 %7, %13 offset:%22\n\tds_read_b32 %8, %14\n\tds_read_b32 %9, %15\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h), "=&v"(y), "=&v"(z)
+      : "v"(p), "v"(q), "v"(r), "v"(s), "v"(at_y), "v"(at_z), "n"(ROW), "n"(2 * ROW), "n"(3 * ROW), "n"(OFF), "n"(OFF + ROW),
+        "n"(OFF + 2 * ROW), "n"(OFF + 3 * ROW)
       : "memory");
 }
 
@@ -314,15 +337,14 @@ struct Chunk {
 //    to it, the others stay whole, and the launch runs them as places fall free.
 //  - Parts under kMinUnits gain nothing.
 // Every wave works it out by itself from the lengths, 64 rows at a time, a row per
-// lane, in doubles (exact below 2^53) for their lane scans.  Returns false where
-// there is nothing for this workgroup.
+// lane.  Returns false where there is nothing for this workgroup.
 template <int KW>
 __device__ __forceinline__ bool plan(const TreeAttnParams &p, int HR, int tree_tiles, Chunk &k) {
   const int lane = threadIdx.x & (kWave - 1);
   struct Row {
     int row, len, start;
     bool bad;
-    uint32_t units;
+    int units;
   };
   auto load = [&](int b0) {
     Row x{};
@@ -333,55 +355,49 @@ __device__ __forceinline__ bool plan(const TreeAttnParams &p, int HR, int tree_t
       x.len = in ? p.len[x.row] : -1;
       x.start = p.width ? p.width[p.group > 0 ? b / p.group : 0] - x.len : 0;
       x.bad = x.len < 0 || x.start < 0 || (long long)x.start + x.len > p.cap;
-      x.units = x.bad ? 0u : (uint32_t)(((x.len + kTile - 1) / kTile + tree_tiles + KW - 1) / KW);
+      x.units = x.bad ? 0 : ((x.len + kTile - 1) / kTile + tree_tiles + KW - 1) / KW;
     }
     return x;
   };
-  Row one = load(0);  // all there is for B <= 64
+  const Row one = load(0);  // all there is for B <= 64
+  auto rows_at = [&](int b0) { return b0 ? load(b0) : one; };
   double total = 0.0;
-  uint32_t longest = 0;
+  int longest = 0;
   bool bad = false;
   for (int b0 = 0; b0 < p.B; b0 += kWave) {
-    const Row x = b0 ? load(b0) : one;
+    const Row x = rows_at(b0);
     bad |= x.bad;
     total += wave_total_f64((double)x.units);
     longest = max(longest, x.units);
   }
-  longest = (uint32_t)wave_max_f32((float)longest) + 1u;  // an upper bound (fp32 may round down by less than one in 2^24)
-  longest += longest >> 20;
-  const double segs = (double)p.B * HR;
-  bad = __any(bad);
-  if (bad || total * HR >= 2147483648.0) {
+  if (__any(bad) || total * HR >= 1073741824.0) {
     if (threadIdx.x == 0) set_status(p.status, SPECDEC_S_LEN_RANGE);
     return false;
   }
-  const double room = p.resident > segs ? (double)p.resident - 0.5 * segs : (double)p.resident;
-  uint32_t u = (uint32_t)(total * HR / room) + 1u;
-  u = u < kMinUnits ? kMinUnits : u;
-  auto parts = [&](uint32_t units) { return (units + u - 1) / u; };
-  if (p.resident > segs) {
-    for (int k = 0; u < longest; ++k) {
-      double n = 0.0;
-      for (int b0 = 0; b0 < p.B; b0 += kWave) n += wave_total_f64((double)parts((b0 ? load(b0) : one).units));
-      if (n * HR <= p.resident) break;
-      u = k < 16 ? u + (u + 7) / 8 : longest;
-    }
+  const int segs = p.B * HR;
+  const float room = p.resident > segs ? (float)p.resident - 0.5f * (float)segs : (float)p.resident;
+  // rounded up past the float's errors: no fewer units than an even share
+  int u = max((int)((float)total * (float)HR / room * 1.00001f) + 1, kMinUnits);
+  auto parts_of = [&](int units) { return (int)((uint32_t)(units + u - 1) / (uint32_t)u); };
+  int all = 0;
+  for (int tries = 0;; ++tries) {
+    all = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kWave) all += wave_total_i32(parts_of(rows_at(b0).units));
+    all *= HR;
+    if (all <= p.resident || p.resident <= segs || !__any(longest > u)) break;
+    u = tries < 16 ? u + (u + 7) / 8 : 1 << 30;
   }
-  // all parts, in order of batch row, segment and key; those of cut segments have slots
-  double all = 0.0;
-  for (int b0 = 0; b0 < p.B; b0 += kWave) all += wave_total_f64((double)parts((b0 ? load(b0) : one).units));
-  const int W = (int)(all * HR);
   // consecutive parts on one XCD (workgroups go to the 8 XCDs in turn), so query
   // blocks that share keys share an L2
-  const int per_xcd = (W + 7) / 8, on_xcd = (int)(blockIdx.x >> 3);
+  const int per_xcd = (all + 7) / 8, on_xcd = (int)(blockIdx.x >> 3);
   const int w = (int)(blockIdx.x & 7) * per_xcd + on_xcd;
-  if (on_xcd >= per_xcd || w >= W) return false;
-  double before = 0.0, slots = 0.0;
+  if (on_xcd >= per_xcd || w >= all) return false;
+  // all parts, in order of batch row, segment and key; those of cut segments have slots
+  int before = 0, slots = 0;
   for (int b0 = 0; b0 < p.B; b0 += kWave) {
-    const Row x = b0 ? load(b0) : one;
-    const uint32_t n = parts(x.units);
-    const double mine = (double)n * HR, cut = n > 1 ? mine : 0.0;
-    const double incl = wave_scan_f64(mine), icut = wave_scan_f64(cut);
+    const Row x = rows_at(b0);
+    const int n = parts_of(x.units), mine = n * HR, cut = n > 1 ? mine : 0;
+    const int incl = wave_scan_i32(mine), icut = wave_scan_i32(cut);
     const unsigned long long hit = __ballot(before + incl > w);
     if (hit) {
       const int at = __builtin_ctzll(hit);
@@ -389,21 +405,21 @@ __device__ __forceinline__ bool plan(const TreeAttnParams &p, int HR, int tree_t
       k.row = __builtin_amdgcn_readlane(x.row, at);
       k.len = __builtin_amdgcn_readlane(x.len, at);
       k.start = __builtin_amdgcn_readlane(x.start, at);
-      const int units = __builtin_amdgcn_readlane((int)x.units, at), np = __builtin_amdgcn_readlane((int)n, at);
-      const int rel = w - (int)(before + lane_f64(incl - mine, at));
-      k.seg = rel / np;
+      const int units = __builtin_amdgcn_readlane(x.units, at), np = __builtin_amdgcn_readlane(n, at);
+      const int rel = w - before - __builtin_amdgcn_readlane(incl - mine, at);
+      k.seg = uniform((int)((uint32_t)rel / (uint32_t)np));
       const int part = rel - k.seg * np;
       // even parts: the first `units % np` are one longer
-      const int each = units / np, longer = units - each * np;
+      const int each = uniform((int)((uint32_t)units / (uint32_t)np)), longer = units - each * np;
       k.unit0 = part * each + min(part, longer);
       k.unit1 = k.unit0 + each + (part < longer);
       k.parts = np;
-      k.slot0 = np > 1 ? (int)(slots + lane_f64(icut - cut, at)) + k.seg * np : 0;
+      k.slot0 = np > 1 ? slots + __builtin_amdgcn_readlane(icut - cut, at) + k.seg * np : 0;
       k.slot = np > 1 ? k.slot0 + part : -1;
       return true;
     }
-    before += lane_f64(incl, kWave - 1);
-    slots += lane_f64(icut, kWave - 1);
+    before += __builtin_amdgcn_readlane(incl, kWave - 1);
+    slots += __builtin_amdgcn_readlane(icut, kWave - 1);
   }
   return false;
 }
@@ -413,10 +429,10 @@ __device__ __forceinline__ bool plan(const TreeAttnParams &p, int HR, int tree_t
 // RT 16-query tiles per wave, RW waves across queries times KW across keys; DHP
 // the head size, or with PAD the next of 64, 128 and 256.
 template <int DT, int DHP, int RT, int RW, int KW, bool PAGED, bool PAD>
-__global__ __launch_bounds__(RW * KW * kWave, attn_waves_per_simd(DT, DHP)) void k_tree_attention(TreeAttnParams p) {
+__global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_direct_wgs(DT, DHP)) void k_tree_attention(TreeAttnParams p) {
   constexpr int NW = RW * KW, NT = NW * kWave;
   constexpr bool SHARED = RW > 1;         // keys pass through LDS, for the waves that share them
-  constexpr bool NEXT = !SHARED && RT == 1;
+  constexpr bool NEXT = !SHARED && RT == 1;  // registers for a second tile
   constexpr int ES = es<DT>();
   constexpr int EL = 16 / ES;             // elements of a 16-byte piece
   constexpr int KS = DHP / (4 * EL);      // contraction steps of S (4 lane groups x EL elements)
@@ -427,9 +443,8 @@ __global__ __launch_bounds__(RW * KW * kWave, attn_waves_per_simd(DT, DHP)) void
   // LDS of the keys: per stage and key wave 32 rows of K, then of V
   constexpr int P = DHP * ES / 16;        // 16-byte pieces of a row
   constexpr int TILE_BYTES = 2 * kTile * P * 16;
-  constexpr int ST = SHARED ? attn_stages(KW * TILE_BYTES) : 1;
+  constexpr int ST = SHARED ? attn_stages(KW * TILE_BYTES) : 4, U = (ST - 1) / 2;
   constexpr int PASS = (kTile * P + RW * kWave - 1) / (RW * kWave);  // wave-loads of K (of V) that a wave makes at most
-  constexpr int PASS_LEAST = kTile * P / (RW * kWave);               // and at least
   constexpr int KEY_BYTES = SHARED ? ST * KW * TILE_BYTES : 0;
   constexpr int O_BYTES = KW > 1 ? NW * RT * 16 * LROW * 4 : 0;
 
@@ -612,8 +627,7 @@ __global__ __launch_bounds__(RW * KW * kWave, attn_waves_per_simd(DT, DHP)) void
     bool up = false;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      top[rt] = fmaxf(fmaxf(fmaxf(s[rt][0][0], s[rt][0][1]), fmaxf(s[rt][0][2], s[rt][0][3])),
-                      fmaxf(fmaxf(s[rt][1][0], s[rt][1][1]), fmaxf(s[rt][1][2], s[rt][1][3]))) * p.scale;
+      top[rt] = max8(s[rt][0], s[rt][1]) * p.scale;
       up |= top[rt] > m[rt] + kSlack;
     }
     if (!__any(up)) return;
@@ -735,63 +749,90 @@ __global__ __launch_bounds__(RW * KW * kWave, attn_waves_per_simd(DT, DHP)) void
     while (tl < t1) step(std::false_type{});
   } else {
     // Keys through LDS, each piece loaded once for the RW waves that share it, by
-    // loads that write LDS directly: ST - 1 tiles are on their way while one is
-    // multiplied, and none of them holds a register.  A wave-load fills 64 slots of
-    // 16 bytes in a row; which piece of its row a slot holds is turned by swz(row),
-    // so that the 16 rows that one read of K touches lie in different banks.  All
-    // waves of the workgroup step together: a step waits for this wave's share of
-    // its tile, then for the others', starts the tile ST - 1 ahead (whose place the
-    // last step has freed) and multiplies.
+    // loads that write LDS directly and hold no register.  A wave-load fills 64
+    // slots of 16 bytes in a row; which piece of its row a slot holds is turned by
+    // swz(row), so that the 16 rows that one read of K touches lie in different
+    // banks.  LDS holds ST >= 2 U + 1 tiles (per key wave) in a ring.  A step
+    // multiplies V of tile i and K of tile i + 1 and starts the loads of tile i + U +
+    // 1; the waves meet every U steps, where the tiles up to i + U must have come and
+    // nobody reads the ones before i any more.  Between, they drift apart, and one's
+    // softmax runs beside another's products.
     const int in_group = rw * kWave + lane;
     auto tile_of = [&](int i) { return t0 + kw + i * KW; };
     const int mine = tile_of(0) < t1 ? (t1 - tile_of(0) + KW - 1) / KW : 0;  // tiles of this key wave
     const int steps = (t1 - t0 + KW - 1) / KW;
-    // The page ids of the next kWindow blocks are kept in LDS: looked up tile by
-    // tile they would return in order with the keys that are on their way.
-    int window = 0;  // first block of it
-    auto fill_window = [&](int tl) {
-      window = (int)fdiv((uint32_t)min(tl * kTile, max(len - 1, 0)), p.page_div);
-      const int n = min(kWindow, (len + p.page - 1) / p.page - window);
+    // The page ids of the next kWindow blocks (as row indexes) are kept in LDS:
+    // looked up tile by tile they would return in order with the keys that are on
+    // their way.
+    int window = 0, filled = 0;  // its first block; the first tile that is not all in it
+    const uint32_t lds0 = lds_offset(s_mem) + kw * TILE_BYTES, hole_at = lds_offset(&s_hole);
+    // The page ids of tiles i0 .. i1 are in the window.  Every wave of the
+    // workgroup comes here, past a barrier: the window moves for all together.
+    auto need_pages = [&](int i0, int i1) {
+      const int first = t0 + i0 * KW, end = min(t0 + (i1 + 1) * KW, cache_tiles);
+      if (!PAGED || first >= end || end <= filled) return;
+      window = (int)fdiv((uint32_t)(first * kTile), p.page_div);
+      const int blocks = (int)fdiv((uint32_t)(len - 1), p.page_div) + 1, n = min(kWindow, blocks - window);
       for (int i = t; i < n; i += NT) {
         const int page = table[window + i];
         const bool in = (uint32_t)page < (uint32_t)p.n_pages;
         if (!in) {
           bad_page = true;
-          lds_set(lds_offset(&s_hole), 1u);
+          lds_set(hole_at, 1u);
         }
-        lds_set(lds_offset(&s_page[i]), in ? (uint32_t)page : 0u);
+        lds_set(lds_offset(&s_page[i]), ((in ? (uint32_t)page : 0u) * H + h) * p.page);
+      }
+      filled = window + n == blocks ? cache_tiles : (window + n) * p.page / kTile;
+      barrier();
+    };
+    static_assert(PASS <= 2, "two rows of K, and of V, per lane and tile");
+    // This lane's rows of the tile to be fetched next: position, block and place in
+    // it, moved on from tile to tile; past the last key the last one is read again.
+    const int by = KW * kTile, by_blocks = PAGED ? (int)fdiv((uint32_t)by, p.page_div) : 0, by_rest = by - by_blocks * p.page;
+    const int end_block = PAGED && len > 0 ? (int)fdiv((uint32_t)(len - 1), p.page_div) : 0;
+    const int end_slot = len - 1 - end_block * p.page;
+    int pos[PASS], blk[PASS], slot[PASS];
+#pragma unroll
+    for (int j = 0; j < PASS; ++j) {
+      pos[j] = tile_of(0) * kTile + (in_group + j * RW * kWave) / P;
+      blk[j] = PAGED ? (int)fdiv((uint32_t)pos[j], p.page_div) : 0;
+      slot[j] = pos[j] - blk[j] * p.page;
+    }
+    // the words of LDS that begin those rows' blocks
+    auto where = [&](uint32_t (&at)[2]) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int y = min(j, PASS - 1);
+        at[j] = lds_offset(s_page) + (PAGED ? (uint32_t)max((pos[y] < len ? blk[y] : end_block) - window, 0) * 4u : 0u);
       }
     };
-    // the last tile whose blocks are all in it
-    auto window_end = [&] {
-      return (int)min((long long)(window + kWindow) * p.page / kTile - 1, (long long)cache_tiles - 1);
-    };
-    auto fetch = [&](int i) {
+    // the loads of tile i, with those words
+    auto fetch = [&](int i, const uint32_t (&page)[2]) {
       const int tl = tile_of(i);
-      const char *kb = static_cast<const char *>(tl < cache_tiles ? p.k_old : p.k_new);
-      const char *vb = static_cast<const char *>(tl < cache_tiles ? p.v_old : p.v_new);
+      const bool is_old = tl < cache_tiles;
+      const char *kb = static_cast<const char *>(is_old ? p.k_old : p.k_new);
+      const char *vb = static_cast<const char *>(is_old ? p.v_old : p.v_new);
       char *to = s_mem + ((i % ST) * KW + kw) * TILE_BYTES + rw * (kWave * 16);
 #pragma unroll
       for (int j = 0; j < PASS; ++j) {
         const int row = (in_group + j * RW * kWave) / P;
-        if (kTile * P % (RW * kWave) != 0 && row >= kTile) break;  // whole waves, where RW is 3 or 6
+        if (kTile * P % (RW * kWave) != 0 && row >= kTile) break;  // whole waves, where RW is 6
         const int piece = (in_group + j * RW * kWave) % P ^ swz<P>(row);
         uint32_t rho;
-        if (tl >= cache_tiles) {
-          rho = new0 + (uint32_t)min((tl - cache_tiles) * kTile + row, N - 1);
-        } else {
-          const uint32_t pos = (uint32_t)min(tl * kTile + row, len - 1);
-          if constexpr (PAGED) {
-            const uint32_t blk = fdiv(pos, p.page_div);
-            rho = (lds_get(lds_offset(s_page) + (blk - (uint32_t)window) * 4u) * H + h) * p.page + (pos - blk * p.page);
-          } else {
-            rho = old0 + pos;
-          }
+        if (!is_old) rho = new0 + (uint32_t)min((tl - cache_tiles) * kTile + row, N - 1);
+        else if constexpr (PAGED) rho = page[j] + (uint32_t)(pos[j] < len ? slot[j] : end_slot);
+        else rho = old0 + (uint32_t)min(pos[j], len - 1);
+        if (i < mine && (!PAD || piece * EL < Dh)) {
+          load_lds(kb + piece * 16 + (size_t)rho * row_bytes, to + j * RW * kWave * 16);
+          load_lds(vb + piece * 16 + (size_t)rho * row_bytes, to + j * RW * kWave * 16 + kTile * P * 16);
         }
-        const size_t src = (size_t)rho * row_bytes + piece * 16;
-        if (!PAD || piece * EL < Dh) {
-          load_lds(kb + src, to + j * RW * kWave * 16);
-          load_lds(vb + src, to + j * RW * kWave * 16 + kTile * P * 16);
+        pos[j] += by;
+        if constexpr (PAGED) {
+          blk[j] += by_blocks;
+          slot[j] += by_rest;
+          const bool next = slot[j] >= p.page;
+          blk[j] += next;
+          slot[j] -= next ? p.page : 0;
         }
       }
     };
@@ -808,12 +849,12 @@ __global__ __launch_bounds__(RW * KW * kWave, attn_waves_per_simd(DT, DHP)) void
       } else {
 #pragma unroll
         for (int s = 0; s < KS; s += 4)
-          lds_read<HALF, 0, 0>(x.k[0][s], x.k[0][s + 1], x.k[0][s + 2], x.k[0][s + 3], x.k[1][s], x.k[1][s + 1],
-                               x.k[1][s + 2], x.k[1][s + 3], a ^ (64u * s), a ^ (64u * (s + 1)), a ^ (64u * (s + 2)),
-                               a ^ (64u * (s + 3)));
+          lds_read<HALF>(x.k[0][s], x.k[0][s + 1], x.k[0][s + 2], x.k[0][s + 3], x.k[1][s], x.k[1][s + 1],
+                         x.k[1][s + 2], x.k[1][s + 3], a ^ (64u * s), a ^ (64u * (s + 1)), a ^ (64u * (s + 2)),
+                         a ^ (64u * (s + 3)));
       }
     };
-    auto read_v = [&](Keys &x, uint32_t tile) {
+    auto read_v = [&](Keys &x, uint32_t tile, const uint32_t (&at)[2], uint32_t (&page)[2]) {
       const uint32_t a = tile + v_at;
       // row g * 4 + i: its turn is (g * 4 + i) & 15, or of two rows of 8 pieces (g * 2 + i / 2) & 7
       constexpr uint32_t T1 = P == 8 ? 0u : 16u, T2 = P == 8 ? 16u : 32u, T3 = P == 8 ? 16u : 48u;
@@ -823,7 +864,8 @@ __global__ __launch_bounds__(RW * KW * kWave, attn_waves_per_simd(DT, DHP)) void
         const uint32_t e = a ^ (16u * d);
         if constexpr (VD == 2) {
           u32x2 y[8];
-          lds_read<HALF, P * 16, 0>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], e, e ^ T1, e ^ T2, e ^ T3);
+          lds_read<HALF, P * 16>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], page[0], page[1], e, e ^ T1, e ^ T2, e ^ T3, at[0],
+                                 at[1]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             x.v[i][0] = y[i][0];
@@ -831,7 +873,8 @@ __global__ __launch_bounds__(RW * KW * kWave, attn_waves_per_simd(DT, DHP)) void
           }
         } else {
           u32x4 y[8];
-          lds_read<HALF, P * 16, 0>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], e, e ^ T1, e ^ T2, e ^ T3);
+          lds_read<HALF, P * 16>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], page[0], page[1], e, e ^ T1, e ^ T2, e ^ T3, at[0],
+                                 at[1]);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -839,33 +882,24 @@ __global__ __launch_bounds__(RW * KW * kWave, attn_waves_per_simd(DT, DHP)) void
         }
       }
     };
-    const uint32_t lds0 = lds_offset(s_mem) + kw * TILE_BYTES, hole_at = lds_offset(&s_hole);
     if constexpr (PAD) {  // pieces past Dh are never written: they read as zeros
       for (int i = t; i < ST * KW * TILE_BYTES / 16; i += NT) reinterpret_cast<u32x4 *>(s_mem)[i] = (u32x4)(0u);
     }
-    // the first window, wherever the part's first tiles lie
-    const bool has_old = PAGED && t0 < cache_tiles;
     load_q();
-    __syncthreads();  // s_hole
-    if (has_old) fill_window(t0);
     if (need_anc) tree_ancestors(N, raw_parent, p.status, s_ptr, s_anc);
-    else __syncthreads();  // the window, and the zeros
+    else __syncthreads();  // s_hole, and the zeros
     settle<DT>(q, p.negate);
-    int filled = has_old ? window_end() : 0x7FFFFFFF;
-    // every wave of the workgroup comes here: the window moves for all together
-    auto next_fetch = [&](int i) {
-      if (PAGED && t0 + i * KW + KW - 1 > filled && t0 + i * KW < cache_tiles) {
-        barrier();
-        fill_window(t0 + i * KW);
-        filled = window_end();
-        if (filled == cache_tiles - 1) filled = 0x7FFFFFFF;
-        barrier();
+    need_pages(0, U);
+#pragma unroll 1
+    for (int i = 0; i <= U; ++i) {
+      uint32_t at[2], page[2] = {0u, 0u};
+      where(at);
+      if constexpr (PAGED) {
+        page[0] = lds_get(at[0]);
+        page[1] = lds_get(at[1]);
       }
-      if (i < mine) fetch(i);
-    };
-    if (filled == cache_tiles - 1) filled = 0x7FFFFFFF;
-#pragma unroll
-    for (int i = 0; i + 1 < ST; ++i) next_fetch(i);
+      fetch(i, page);
+    }
     // keys of a tile that exist: all but the last ones, unless some page was bad
     auto existing_keys = [&](int tl, bool hole) -> uint32_t {
       const int n = tl < cache_tiles ? len - tl * kTile : N - (tl - cache_tiles) * kTile;
@@ -877,65 +911,60 @@ __global__ __launch_bounds__(RW * KW * kWave, attn_waves_per_simd(DT, DHP)) void
       }
       return vm;
     };
-    Keys x;
     Scores s;
-    u32x4 w[RT];
-    // A step multiplies V of tile i and, where three tiles fit LDS, already K of
-    // tile i + 1: its scores need nothing of the softmax that goes on meanwhile.
-    constexpr int AHEAD = ST > 2 ? 1 : 0;
+    auto tile_at = [&](int i) { return lds0 + (uint32_t)((i % ST) * KW * TILE_BYTES); };
     auto new_scores = [&](int i, bool hole) {
       const int tl = tile_of(i);
-      read_k(x, lds0 + (uint32_t)((i % ST) * KW * TILE_BYTES));
+      Keys x;
+      read_k(x, tile_at(i));
       scores(x, s);
       const uint32_t vm = existing_keys(tl, hole);
       if (tl >= cache_tiles || vm != 0xFFFFFFFFu) mask_scores(s, tl, vm);
+      raise(s);
     };
-    if constexpr (AHEAD == 1) {
-      if (ST - 2 < mine) wait_loads<2 * PASS_LEAST * (ST - 2)>();
-      else wait_loads<0>();
-      barrier();
-      if (mine > 0) {
-        new_scores(0, uniform((int)lds_get(hole_at)) != 0);
-        raise(s);
-      }
+    bool hole = false;
+    int i = 0, due = 0;
+    auto meet = [&] {
+      due += U;
+      wait_loads<0>();  // this wave's share of the tiles up to i + U
+      barrier();        // the others', and all are past the tiles before i
+      hole = uniform((int)lds_get(hole_at)) != 0;
+      need_pages(i + U + 1, i + 2 * U);
+    };
+    meet();
+    if (mine > 0) new_scores(0, hole);
+    for (; tile_of(i + 1) < whole_tiles; ++i) {  // whole tiles, and one after them
+      if (i == due) meet();
+      if (hole) break;
+      Keys x;
+      u32x4 w[RT];
+      uint32_t at[2], page[2];
+      where(at);
+      weights(s, w);
+      __builtin_amdgcn_sched_barrier(0);
+      read_v(x, tile_at(i), at, page);
+      products(x, s, w);
+      fetch(i + U + 1, page);
+      __builtin_amdgcn_sched_barrier(0);  // V's registers are free before K's fill
+      read_k(x, tile_at(i + 1));
+      scores(x, s);
+      raise(s);
     }
-    for (int i = 0; i < steps; ++i) {
-      // this wave's loads of tile i + AHEAD: those of the tiles after it may be out
-      if (i + ST - 2 < mine) wait_loads<2 * PASS_LEAST * (ST - 2 - AHEAD)>();
-      else wait_loads<0>();
-      barrier();
-      const bool hole = uniform((int)lds_get(hole_at)) != 0;
-      next_fetch(i + ST - 1);
-      const uint32_t tile = lds0 + (uint32_t)((i % ST) * KW * TILE_BYTES);
-      if (AHEAD == 1 && tile_of(i + 1) < whole_tiles && !hole) {
-        Scores next;
-        read_k(x, lds0 + (uint32_t)(((i + 1) % ST) * KW * TILE_BYTES));
-        scores(x, next);
-        weights(s, w);
-        __builtin_amdgcn_sched_barrier(0);  // K's registers are free before V's fill
-        read_v(x, tile);
-        products(x, s, w);
-        raise(next);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int kt = 0; kt < 2; ++kt) s[rt][kt] = next[rt][kt];
-      } else if (i < mine) {
-        const int tl = tile_of(i);
-        if constexpr (AHEAD == 0) {
-          new_scores(i, hole);
-          raise(s);
-        }
-        read_v(x, tile);
-        const uint32_t vm = existing_keys(tl, hole);
-        if (tl >= cache_tiles || vm != 0xFFFFFFFFu) mask_values(x, tl, vm);
-        weights(s, w);
-        products(x, s, w);
-        if (AHEAD == 1 && i + 1 < mine) {
-          new_scores(i + 1, hole);
-          raise(s);
-        }
-      }
+    for (; i < steps; ++i) {
+      if (i == due) meet();
+      if (i >= mine) continue;
+      Keys x;
+      u32x4 w[RT];
+      uint32_t at[2], page[2];
+      where(at);
+      weights(s, w);
+      read_v(x, tile_at(i), at, page);
+      fetch(i + U + 1, page);
+      const int tl = tile_of(i);
+      const uint32_t vm = existing_keys(tl, hole);
+      if (tl >= cache_tiles || vm != 0xFFFFFFFFu) mask_values(x, tl, vm);
+      products(x, s, w);
+      if (i + 1 < mine) new_scores(i + 1, hole);
     }
     __syncthreads();  // the keys' LDS is free
   }
@@ -1097,11 +1126,10 @@ static hipError_t launch_attn_dh(const TreeAttnParams &p, const AttnShape &a, hi
     if (a.rt == 2) return launch_attn<DT, DHP, 2, 8, 1>(p, s);
     if (a.rw == 6) return launch_attn<DT, DHP, 1, 6, 1>(p, s);
   }
-  if constexpr (attn_waves_per_simd(DT, DHP) == 2) {
-    if (a.rw == 4) return launch_attn<DT, DHP, 1, 4, 2>(p, s);
+  if constexpr (attn_shared(DT, DHP)) {
+    if constexpr (attn_share_keys(DT, DHP) == 2)
+      if (a.rw == 4) return launch_attn<DT, DHP, 1, 4, 2>(p, s);
     if (a.rw == 8) return launch_attn<DT, DHP, 1, 8, 1>(p, s);
-  } else {
-    if (a.rw == 4) return launch_attn<DT, DHP, 1, 4, 1>(p, s);
   }
   return hipErrorInvalidValue;
 }

@@ -34,6 +34,23 @@ __device__ __forceinline__ double wave_scan_f64(double x) {
   return x;
 }
 
+// Inclusive prefix sums and the sum of 32-bit integers over the wave's lanes, as
+// wave_scan_f64.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ int dpp_i32(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, ROW_MASK, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan_i32(int x) {
+  x += dpp_i32<0x111, 0xF>(x);
+  x += dpp_i32<0x112, 0xF>(x);
+  x += dpp_i32<0x114, 0xF>(x);
+  x += dpp_i32<0x118, 0xF>(x);
+  x += dpp_i32<0x142, 0xA>(x);
+  x += dpp_i32<0x143, 0xC>(x);
+  return x;
+}
+__device__ __forceinline__ int wave_total_i32(int x) { return __builtin_amdgcn_readlane(wave_scan_i32(x), kWave - 1); }
+
 __device__ __forceinline__ double lane_f64(double x, int lane) {
   const long long v = __double_as_longlong(x);
   const int lo = __builtin_amdgcn_readlane((int)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);

@@ -819,6 +819,7 @@ AttnShape attn_shape(int dtype, int Dh, int M) {
     a.kw = 2;
   } else if (most == 2 && (M <= 96 || (M > 128 && M <= 192))) {
     a.rw = 6;  // blocks of 96 rows: the least rows left over
+    a.kw = 2;
   } else {
     a.rw = 8;
     a.rt = most == 2 && M > 128 ? 2 : 1;
@@ -834,9 +835,11 @@ int attn_resident(int dtype, const AttnShape &a) {
 
 // A segment in several parts has less than two parts per resident workgroup's
 // share of the work, so all of them have less than twice the resident ones.
-static size_t attn_workspace(int dtype, const sd::AttnShape &a, size_t &slots) {
-  slots = 2 * (size_t)sd::attn_resident(dtype, a);
-  return slots * (sd::kAtomicLine + a.part_bytes());
+static size_t attn_workspace(int dtype, const sd::AttnShape &a, size_t &counters, size_t &partial) {
+  const size_t resident = (size_t)sd::attn_resident(dtype, a), slots = 2 * resident;
+  counters = slots * sd::kAtomicLine;
+  partial = counters + (resident + 1) * 16;
+  return partial + slots * a.part_bytes();
 }
 
 EXPORT size_t specdec_tree_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, int head_dim) {
@@ -846,8 +849,8 @@ EXPORT size_t specdec_tree_attention_workspace_bytes(int B, int N, int q_heads, 
   size_t most = 0;
   for (int dt = 0; dt < 3; ++dt) {
     const sd::AttnShape a = sd::attn_shape(dt, head_dim, N * (q_heads / kv_heads));
-    size_t slots;
-    const size_t n = attn_workspace(dt, a, slots);
+    size_t counters, partial;
+    const size_t n = attn_workspace(dt, a, counters, partial);
     most = n > most ? n : most;
   }
   return most;
@@ -895,10 +898,10 @@ static int attention(sd::TreeAttnParams &p, const void *kv, size_t old_bytes, in
   if (segs >= (1LL << 30)) return SPECDEC_E_ARG;
   p.grid = (int)(segs < p.resident ? p.resident : segs + p.resident + 7) / 8 * 8;
   if (p.grid < p.resident) p.grid += 8;
-  size_t slots;
-  const size_t need = attn_workspace(dtype, a, slots), counters = slots * sd::kAtomicLine, partial = need - counters;
+  size_t counters, partial;
+  const size_t need = attn_workspace(dtype, a, counters, partial);
   if (!ws || ws_bytes < need || reinterpret_cast<uintptr_t>(ws) % 16 != 0) return SPECDEC_E_WORKSPACE;
-  if (partial >= (1u << 31)) return SPECDEC_E_ARG;
+  if (need - partial >= (1u << 31)) return SPECDEC_E_ARG;
   p.q = q;
   p.out = out;
   for (int k = 0; k < 3; ++k) {
@@ -912,8 +915,9 @@ static int attention(sd::TreeAttnParams &p, const void *kv, size_t old_bytes, in
   p.scale = fmaxf((float)(fabs((double)scale) * 1.44269504088896340736), 1.17549435e-38f);
   p.negate = scale < 0.0f;
   p.counters = static_cast<unsigned int *>(ws);
-  p.partial = static_cast<char *>(ws) + counters;
-  p.partial_bytes = (int)partial;
+  p.cuts = reinterpret_cast<int4 *>(static_cast<char *>(ws) + counters);
+  p.partial = static_cast<char *>(ws) + partial;
+  p.partial_bytes = (int)(need - partial);
   p.page_div = sd::host_fast_div((uint32_t)(p.page > 0 ? p.page : 1));
   p.g_div = sd::host_fast_div((uint32_t)p.G);
   hipStream_t s = as_stream(stream);

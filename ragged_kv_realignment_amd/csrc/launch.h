@@ -81,7 +81,8 @@ struct TreeAttnParams {
   int B, N, H, G, Dh;
   float scale;                           // its size times log2(e)
   bool negate;                           // it was negative
-  unsigned int *counters;                // workspace: a line per workgroup, zero between calls
+  unsigned int *counters;                // workspace: a line per part, zero between calls
+  int4 *cuts;                            // the number of segments in several parts, then (first part's slot, parts, row, segment)
   void *partial;
   int partial_bytes, blocks, resident, grid;  // query blocks per head, workgroups
   int32_t *status;

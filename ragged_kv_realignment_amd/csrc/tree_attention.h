@@ -29,8 +29,9 @@
 // keys of a segment (few rows).  Waves that share keys take them through LDS.
 //
 // A segment that is cut into parts (see plan) leaves (max, sum, O) of each in the
-// workspace, and the last workgroup to arrive adds them in part order, so results
-// do not depend on timing.  The order of completion uses the same scheme as
+// workspace.  Of up to 32 query rows, the last workgroup to arrive adds them; of
+// more, a second kernel does.  Either adds in part order, so results do not depend
+// on timing.  The order of completion in the first case uses the same scheme as
 // verification: sums stored past the non-coherent L2 (sc1), completed (vmcnt)
 // before the count, loaded only after the count has returned.
 #pragma once
@@ -139,13 +140,10 @@ __device__ __forceinline__ f32x4 ld_f4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kCoherentPolicy));
 }
 
-// Elements e .. e+7 (a, then d) of query row `row` of (b, h), unless its node
-// is not part of the tree (anc: the nodes' ancestor bits).
+// Elements e .. e+7 (a, then d) of query row `row` of (b, h), times f.
 template <int DT>
-__device__ __forceinline__ void store_out(const TreeAttnParams &p, int b, int h, int row, int e, f32x4 a, f32x4 d, float f,
-                                          const uint32_t (*anc)[kMaxNodes / 32]) {
+__device__ __forceinline__ void write_out(const TreeAttnParams &p, int b, int h, int row, int e, f32x4 a, f32x4 d, float f) {
   const int n = (int)fdiv((uint32_t)row, p.g_div), gq = row - n * p.G;
-  if (!(anc[n][0] & 1u)) return;
   char *dst = static_cast<char *>(p.out) + ((int64_t)b * p.os[0] + (int64_t)n * p.os[1] +
                                             (int64_t)(h * p.G + gq) * p.os[2] + e) * es<DT>();
   a *= f;
@@ -157,6 +155,14 @@ __device__ __forceinline__ void store_out(const TreeAttnParams &p, int b, int h,
     *reinterpret_cast<u32x4 *>(dst) =
         u32x4{pack2<DT>(a[0], a[1]), pack2<DT>(a[2], a[3]), pack2<DT>(d[0], d[1]), pack2<DT>(d[2], d[3])};
   }
+}
+
+// The same unless the row's node is not part of the tree (anc: the nodes'
+// ancestor bits).
+template <int DT>
+__device__ __forceinline__ void store_out(const TreeAttnParams &p, int b, int h, int row, int e, f32x4 a, f32x4 d, float f,
+                                          const uint32_t (*anc)[kMaxNodes / 32]) {
+  if (anc[fdiv((uint32_t)row, p.g_div)][0] & 1u) write_out<DT>(p, b, h, row, e, a, d, f);
 }
 
 // The values of V that are not finite, of the nodes of tiles [t0, t1) that query
@@ -325,6 +331,7 @@ struct Chunk {
   int b, seg, row, len, start;
   int unit0, unit1;
   int slot, slot0, parts;  // slot -1: the whole segment
+  int cut, cuts;           // its number among the segments in several parts; theirs (known to part 0)
 };
 
 // The split.  A segment (batch row, KV head, query block) is cut into parts of at
@@ -372,6 +379,7 @@ __device__ __forceinline__ bool plan(const TreeAttnParams &p, int HR, int tree_t
   }
   if (__any(bad) || total * HR >= 1073741824.0) {
     if (threadIdx.x == 0) set_status(p.status, SPECDEC_S_LEN_RANGE);
+    if (threadIdx.x == 0 && blockIdx.x == 0) p.cuts[0].x = 0;
     return false;
   }
   const int segs = p.B * HR;
@@ -393,7 +401,10 @@ __device__ __forceinline__ bool plan(const TreeAttnParams &p, int HR, int tree_t
   const int w = (int)(blockIdx.x & 7) * per_xcd + on_xcd;
   if (on_xcd >= per_xcd || w >= all) return false;
   // all parts, in order of batch row, segment and key; those of cut segments have slots
-  int before = 0, slots = 0;
+  k.cuts = 0;
+  if (w == 0)
+    for (int b0 = 0; b0 < p.B; b0 += kWave) k.cuts += HR * __popcll(__ballot(parts_of(rows_at(b0).units) > 1));
+  int before = 0, slots = 0, cuts = 0;
   for (int b0 = 0; b0 < p.B; b0 += kWave) {
     const Row x = rows_at(b0);
     const int n = parts_of(x.units), mine = n * HR, cut = n > 1 ? mine : 0;
@@ -416,8 +427,10 @@ __device__ __forceinline__ bool plan(const TreeAttnParams &p, int HR, int tree_t
       k.parts = np;
       k.slot0 = np > 1 ? slots + __builtin_amdgcn_readlane(icut - cut, at) + k.seg * np : 0;
       k.slot = np > 1 ? k.slot0 + part : -1;
+      k.cut = cuts + HR * __popcll(__ballot(n > 1) & ((1ull << at) - 1ull)) + k.seg;
       return true;
     }
+    cuts += HR * __popcll(__ballot(n > 1));
     before += __builtin_amdgcn_readlane(incl, kWave - 1);
     slots += __builtin_amdgcn_readlane(icut, kWave - 1);
   }
@@ -465,6 +478,10 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
   // The split of the work (see plan).  Every wave finds it from the lengths.
   Chunk k;
   if (!plan<KW>(p, HR, tree_tiles, k)) return;
+  if constexpr (SHARED) {  // for the kernel that joins the parts
+    if (threadIdx.x == 0 && k.cuts >= 0 && blockIdx.x == 0) p.cuts[0].x = k.cuts;
+    if (threadIdx.x == 0 && k.slot >= 0 && k.slot == k.slot0) p.cuts[1 + k.cut] = int4{k.slot0, k.parts, k.b, k.seg};
+  }
   const int b = k.b, h = k.seg / RB, rb = k.seg - h * RB, r = k.row, len = k.len, start = k.start;
   const int cache_tiles = (len + kTile - 1) / kTile, tiles = cache_tiles + tree_tiles;
   const int t0 = k.unit0 * KW, t1 = min(tiles, k.unit1 * KW);
@@ -885,10 +902,7 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
     if constexpr (PAD) {  // pieces past Dh are never written: they read as zeros
       for (int i = t; i < ST * KW * TILE_BYTES / 16; i += NT) reinterpret_cast<u32x4 *>(s_mem)[i] = (u32x4)(0u);
     }
-    load_q();
-    if (need_anc) tree_ancestors(N, raw_parent, p.status, s_ptr, s_anc);
-    else __syncthreads();  // s_hole, and the zeros
-    settle<DT>(q, p.negate);
+    __syncthreads();  // s_hole, and the zeros
     need_pages(0, U);
 #pragma unroll 1
     for (int i = 0; i <= U; ++i) {
@@ -900,6 +914,9 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
       }
       fetch(i, page);
     }
+    load_q();
+    if (need_anc) tree_ancestors(N, raw_parent, p.status, s_ptr, s_anc);
+    settle<DT>(q, p.negate);
     // keys of a tile that exist: all but the last ones, unless some page was bad
     auto existing_keys = [&](int tl, bool hole) -> uint32_t {
       const int n = tl < cache_tiles ? len - tl * kTile : N - (tl - cache_tiles) * kTile;
@@ -999,9 +1016,18 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
       store_out<DT>(p, b, h, row, e, a, d, 1.0f / sum, s_anc);
     } else {
       const uint32_t off = slot + (uint32_t)(brow * LROW) * 4u;
-      st_f4(wsr, off + (uint32_t)e * 4u, a);
-      st_f4(wsr, off + (uint32_t)e * 4u + 16u, d);
-      if (e == 0) st_f4(wsr, off + DHP * 4u, f32x4{mx, sum, 0.0f, 0.0f});
+      if constexpr (SHARED) {
+        char *to = static_cast<char *>(p.partial) + off;
+        *reinterpret_cast<f32x4 *>(to + e * 4) = a;
+        *reinterpret_cast<f32x4 *>(to + e * 4 + 16) = d;
+        // a sum below zero says that the node is not part of the tree
+        const bool out = need_anc && !(s_anc[fdiv((uint32_t)row, p.g_div)][0] & 1u);
+        if (e == 0) *reinterpret_cast<f32x4 *>(to + DHP * 4) = f32x4{mx, out ? -1.0f : sum, 0.0f, 0.0f};
+      } else {
+        st_f4(wsr, off + (uint32_t)e * 4u, a);
+        st_f4(wsr, off + (uint32_t)e * 4u + 16u, d);
+        if (e == 0) st_f4(wsr, off + DHP * 4u, f32x4{mx, sum, 0.0f, 0.0f});
+      }
     }
   };
   if constexpr (KW == 1) {
@@ -1057,7 +1083,7 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
       finish(brow, e, a, d, mx, sum);
     }
   }
-  if (k.slot < 0) return;
+  if (SHARED || k.slot < 0) return;
 
   // One of several workgroups of the segment: the last to arrive adds them.
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -1102,6 +1128,47 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
   }
 }
 
+// Joins the parts of cut segments where those are of many rows: one workgroup for
+// 256 pieces (of 8 elements) of a segment's rows, added in part order.  (The last
+// part's workgroup would take 60 us for 16 parts of 256 rows by itself, this
+// kernel under 10 with its launch; for up to 32 rows the join in the kernel above
+// is quicker than a second launch.)
+template <int DT, int DHP>
+__global__ __launch_bounds__(kBlock) void k_tree_join(TreeAttnParams p, int rows) {
+  if ((int)blockIdx.x >= p.cuts[0].x) return;
+  const int4 cut = p.cuts[1 + blockIdx.x];
+  constexpr int PIECES = DHP / 8, LROW = DHP + 4, NB = 4;
+  const int i = (int)(blockIdx.y * kBlock + threadIdx.x), e = i % PIECES * 8, brow = i / PIECES;
+  const int h = cut.w / p.blocks, row = (cut.w - h * p.blocks) * rows + brow;
+  if (brow >= rows || row >= p.N * p.G || e >= p.Dh) return;
+  const size_t part_floats = (size_t)rows * LROW;
+  const float *from = static_cast<const float *>(p.partial) + cut.x * part_floats + (size_t)brow * LROW;
+  f32x4 a = (f32x4)(0.0f), d = (f32x4)(0.0f);
+  float mx = kLow, sum = 0.0f;
+  bool out = false;
+  for (int j0 = 0; j0 < cut.y; j0 += NB) {
+    f32x4 ml[NB], pa[NB], pd[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const float *at = from + min(j0 + j, cut.y - 1) * part_floats;
+      ml[j] = *reinterpret_cast<const f32x4 *>(at + DHP);
+      pa[j] = *reinterpret_cast<const f32x4 *>(at + e);
+      pd[j] = *reinterpret_cast<const f32x4 *>(at + e + 4);
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      if (j0 + j >= cut.y) break;
+      out |= ml[j][1] < 0.0f;
+      const float up = fmaxf(mx, ml[j][0]), fo = __builtin_amdgcn_exp2f(mx - up), fn = __builtin_amdgcn_exp2f(ml[j][0] - up);
+      a = a * fo + pa[j] * fn;
+      d = d * fo + pd[j] * fn;
+      sum = sum * fo + ml[j][1] * fn;
+      mx = up;
+    }
+  }
+  if (!out) write_out<DT>(p, cut.z, h, row, e, a, d, 1.0f / sum);
+}
+
 template <int DT, int DHP, int RT, int RW, int KW>
 static hipError_t launch_attn(const TreeAttnParams &p, hipStream_t s) {
   const dim3 grid((unsigned)p.grid), block(RW * KW * kWave);
@@ -1113,6 +1180,13 @@ static hipError_t launch_attn(const TreeAttnParams &p, hipStream_t s) {
     hipLaunchKernelGGL((k_tree_attention<DT, DHP, RT, RW, KW, false, false>), grid, block, 0, s, p);
   else
     hipLaunchKernelGGL((k_tree_attention<DT, DHP, RT, RW, KW, false, true>), grid, block, 0, s, p);
+  if constexpr (RW > 1) {
+    constexpr int kRows = RW * RT * 16;
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const dim3 parts((unsigned)min((long)p.resident, (long)p.B * p.H * p.blocks), (kRows * (DHP / 8) + kBlock - 1) / kBlock);
+    hipLaunchKernelGGL((k_tree_join<DT, DHP>), parts, dim3(kBlock), 0, s, p, kRows);
+  }
   return hipGetLastError();
 }
 
@@ -1124,7 +1198,7 @@ static hipError_t launch_attn_dh(const TreeAttnParams &p, const AttnShape &a, hi
   if constexpr (kMost == 2) {
     if (a.rw == 1) return launch_attn<DT, DHP, 2, 1, 4>(p, s);
     if (a.rt == 2) return launch_attn<DT, DHP, 2, 8, 1>(p, s);
-    if (a.rw == 6) return launch_attn<DT, DHP, 1, 6, 1>(p, s);
+    if (a.rw == 6) return launch_attn<DT, DHP, 1, 6, 2>(p, s);
   }
   if constexpr (attn_shared(DT, DHP)) {
     if constexpr (attn_share_keys(DT, DHP) == 2)

@@ -834,12 +834,15 @@ int attn_resident(int dtype, const AttnShape &a) {
 }  // namespace sd
 
 // A segment in several parts has less than two parts per resident workgroup's
-// share of the work, so all of them have less than twice the resident ones.
+// share of the work, so all of them have less than twice the resident ones.  The
+// counters and cuts lie at the same place for every type and shape, sized for the
+// most resident workgroups (two a CU): calls of any of them may take turns on one
+// workspace, and none writes its partial results over another's zeroed counters.
 static size_t attn_workspace(int dtype, const sd::AttnShape &a, size_t &counters, size_t &partial) {
-  const size_t resident = (size_t)sd::attn_resident(dtype, a), slots = 2 * resident;
-  counters = slots * sd::kAtomicLine;
-  partial = counters + (resident + 1) * 16;
-  return partial + slots * a.part_bytes();
+  const size_t most = 2 * (size_t)sd::device_cus();
+  counters = 2 * most * sd::kAtomicLine;
+  partial = counters + (most + 1) * 16;
+  return partial + 2 * (size_t)sd::attn_resident(dtype, a) * a.part_bytes();
 }
 
 EXPORT size_t specdec_tree_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, int head_dim) {

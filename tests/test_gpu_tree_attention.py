@@ -337,6 +337,137 @@ def test_attention_streams(sd):
             assert torch.equal(x, w)
 
 
+# Query rows per KV head on both sides of every change of tiling, with a row long
+# enough to be split; sizes of heads that fill their tiles and that do not.
+@pytest.mark.parametrize("dt,Dh", [(BF16, 128), (F16, 72), (F16, 64), (BF16, 256), (F32, 64), (F32, 100), (F32, 200)])
+def test_attention_every_tiling(sd, dt, Dh):
+    for k, (N, G) in enumerate([(16, 1), (17, 1), (8, 4), (33, 1), (16, 4), (13, 5), (24, 4), (97, 1), (32, 4), (43, 3),
+                                (48, 4), (193, 1), (64, 4), (51, 7)]):
+        store, page = [("paged", 16), ("rect", 0), ("paged", 1), ("pool", 0), ("paged", 5), ("group", 0)][k % 6]
+        say("tiling", dt, Dh, N, G, store, page)
+        Case(sd, 400 + k, dt, store, [2531, 1, 0, 130], N, 1, G, Dh, page, L=1, layer=0, used=[N, max(1, N - 5), 1, N],
+             wide=k % 2 == 0).check(sd)
+
+
+def test_attention_shared_keys_pages_past_the_window(sd):
+    """More blocks of a row than a workgroup looks up at once."""
+    for dt, N, G, page in ((BF16, 40, 1, 1), (F16, 24, 4, 1), (BF16, 100, 1, 2)):
+        say("past the window", dt, N, G, page)
+        Case(sd, 71, dt, "paged", [5003, 1025, 1024, 1023], N, 1, G, 64, page, L=1, layer=0).check(sd)
+    # few segments beside many, so that parts are longer than the window
+    say("whole long rows")
+    Case(sd, 72, BF16, "paged", [1400] * 8, 40, 40, 1, 64, 1, L=1, layer=0, used=[3] * 8).check(sd)
+
+
+@pytest.mark.parametrize("dt,N,G", [(BF16, 40, 1), (F16, 24, 4), (BF16, 100, 1), (BF16, 64, 4), (F32, 70, 1)])
+def test_attention_shared_keys_bad_pages(sd, dt, N, G):
+    """Bad pages under keys that waves share: their positions take no part, in whichever tile they lie."""
+    for at in ((1,), (0, 2, 3), (5, 9, 30)):
+        for bad in (-1, 1 << 30):
+            c = Case(sd, 73, dt, "paged", [20, 500], N, 1, G, 64, 16, L=1, layer=0)
+            keep = torch.ones(500, dtype=torch.bool)
+            for k in at:
+                c.cache.block_table[int(c.rows[1]), k] = bad
+                keep[k * 16:k * 16 + 16] = False
+            say("bad pages", dt, N, G, at, bad)
+            st = torch.zeros(1, dtype=torch.int32, device="cuda")
+            out = torch.full((2, N, G, 64), 7.0, dtype=dt)
+            got = c.call(sd, out=out.cuda(), status=st)
+            assert int(st) == sd.S_LEN_RANGE
+            k, v = c.old[1]
+            c.old[1] = (k[:, keep], v[:, keep])
+            want, tol = c.want(out)
+            assert bool(((got.cpu().double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dt,N,G", [(BF16, 40, 2), (F16, 96, 1), (BF16, 65, 4), (F32, 50, 1)])
+def test_attention_split_rows_with_values_that_are_not_finite(sd, dt, N, G):
+    """The last part of a split row holds the tree: its branch that overflowed, and nodes that are not used."""
+    c = Case(sd, 79, dt, "paged", [6000], N, 1, G, 64, 16, L=1, layer=0, used=[N - 3])
+    parent = np.full(N, -1, np.int32)
+    parent[1:N - 3] = [0, 0] + [i - 2 for i in range(3, N - 3)]
+    c.parent[:] = parent
+    c.kv_new[0, 1, 0, 0, 9, 3] = -float("inf")
+    out = torch.full((1, N, G, 64), 7.0, dtype=dt)
+    got = c.call(sd, out=out.cuda()).cpu()
+    c.kv_new[0, 1, 0, 0, 9, 3] = 0.0
+    want, tol = c.want(out)
+    lines = T.lines(parent)
+    hit = torch.tensor([9 in line for line in lines])
+    assert bool((got[0, hit][:, :, 3] == -float("inf")).all())
+    got[0, hit, :, 3] = 0.0
+    want[0, hit, :, 3] = 0.0
+    assert bool(((got.double() - want).abs() <= tol).all())
+
+
+def test_attention_many_rows(sd):
+    """Rows past one wave's lanes, up to the most: none, some and all of them split."""
+    rng = np.random.default_rng(5)
+    for B, N, G, lens in ((65, 3, 2, [900] * 65), (130, 5, 1, [int(x) for x in rng.integers(0, 200, 130)]),
+                          (1024, 1, 1, [int(x) for x in rng.integers(0, 9, 1024)]),
+                          (129, 34, 1, [3000, *[1] * 127, 5000]), (200, 2, 1, [*[0] * 199, 30000])):
+        say("many rows", B, N, G)
+        Case(sd, 83, BF16, "paged", lens, N, 1, G, 64, 16, L=1, layer=0, used=[1 + b % N for b in range(B)]).check(sd)
+
+
+def test_attention_types_in_turn_on_one_workspace(sd):
+    """Types that split the same rows in different ways take turns on one workspace."""
+    for N, G, Dh in ((20, 1, 128), (40, 1, 256), (12, 2, 128)):
+        ws = sd.tree_attention_workspace(3, N, 2 * G, 2, Dh)
+        cases = [Case(sd, 89, dt, "paged", [7000, 5, 2000], N, 2, G, Dh, 16, L=1, layer=0) for dt in (BF16, F32, F16)]
+        want = [c.check(sd) for c in cases]
+        for k in (1, 0, 1, 2, 1, 1, 0, 2):
+            say("types in turn", N, G, Dh, k)
+            assert torch.equal(cases[k].check(sd, ws=ws), want[k])
+
+
+def test_attention_scale_of_zero(sd):
+    """Every weight alike: the mean of the values."""
+    for N in (6, 40):
+        Case(sd, 97, BF16, "rect", [300, 64], N, 2, 2, 64, L=1, layer=0).check(sd, scale=0.0)
+
+
+@pytest.mark.parametrize("N,G,Dh", [(6, 2, 128), (40, 1, 64)])
+def test_attention_graph_follows_the_lengths(sd, N, G, Dh):
+    """A captured call plans anew from the lengths of each replay: split, whole, and refused."""
+    c = Case(sd, 101, BF16, "paged", [6000, 100], N, 1, G, Dh, 16, L=1, layer=0)
+    ws = sd.tree_attention_workspace(2, N, G, 1, Dh)
+    q, new, parent, rows = c.q.cuda(), c.kv_new.cuda(), dev(c.parent), dev(c.rows)
+    out = torch.full_like(q, 7.0)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call():
+        sd.tree_attention(q, c.cache, 0, new, parent, rows=rows, ws=ws, out=out, status=st)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    old, at = list(c.old), [int(r) for r in c.rows]
+    for lens in ((6000, 100), (0, 100), (31, 0), (5000, 99), (-1, 5), (6000, 100)):
+        say("replay", lens)
+        for r, n in zip(at, lens):
+            c.cache.len[r] = n
+        out.fill_(7.0)
+        st.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.cpu()
+        if min(lens) < 0:
+            assert int(st) == sd.S_LEN_RANGE and bool((got == 7.0).all())
+            continue
+        assert int(st) == 0
+        c.old = [(k[:, :n], v[:, :n]) for (k, v), n in zip(old, lens)]
+        want, tol = c.want(torch.full_like(got, 7.0))
+        assert bool(((got.double() - want).abs() <= tol).all())
+        call()
+        assert torch.equal(out.cpu(), got)
+
+
 # ------------------------------------------------------------ a round, together
 
 def _round(sd, s, ws, keep):

@@ -16,6 +16,7 @@
 // it is followed from the root.
 #include <math.h>
 #include <limits.h>
+#include <atomic>
 #include "coherent.h"
 #include "device_common.h"
 #include "launch.h"
@@ -295,9 +296,13 @@ __global__ __launch_bounds__(NT) void k_verify_greedy(GreedyParams p, int splits
 }
 
 int device_cus() {
+  // a launch is about as short as the query: each device is asked once
+  static std::atomic<int> known[64];
   int dev = 0, cus = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return 256;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 256;
+  if (dev < 64 && (cus = known[dev].load(std::memory_order_relaxed)) > 0) return cus;
   if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) return 256;
+  if (dev < 64) known[dev].store(cus, std::memory_order_relaxed);
   return cus;
 }
 

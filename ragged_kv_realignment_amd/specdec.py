@@ -639,6 +639,13 @@ def pool_admit(pool, sched, queue, admitted=None, n_admitted=None, status=None):
 
 # ---------------------------------------------------------- trees of drafts
 
+# These calls are short beside the time Python takes to check their arguments, so
+# each looks its tensors over in one expression first and names what is wrong only
+# where that fails.
+
+_I32 = torch.int32
+
+
 def _on(dev, *named):
     """Every given tensor is on `dev` (the kernels dereference all of them there)."""
     for t, n in named:
@@ -646,24 +653,41 @@ def _on(dev, *named):
             raise ValueError("%s must be on %s" % (n, dev))
 
 
+def _is(t, dtype, shape, at):
+    """A contiguous tensor of this type and shape on GPU `at`."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == at and t.is_contiguous()
+
+
 def _ints(shape, dev, *named):
     """Required contiguous int32 tensors of one shape on `dev`."""
+    at = -2 if dev.index is None else dev.index
     for t, n in named:
-        _need(t, n, torch.int32)
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError("%s must have shape %s" % (n, list(shape)))
-    _on(dev, *named)
+        if t is None or not _is(t, _I32, shape, at):
+            _need(t, n, _I32)
+            if tuple(t.shape) != tuple(shape):
+                raise ValueError("%s must have shape %s" % (n, list(shape)))
+            _on(dev, (t, n))
 
 
-def _launch(dev, name, *args):
-    """Calls entry point `name` on `dev`, on torch's current stream there."""
-    stream = torch._C._cuda_getCurrentRawStream(dev.index)
-    if dev.index == torch.cuda.current_device():
-        rc = getattr(lib(), name)(*args, stream)
+def _launch(at, name, *args):
+    """Calls entry point `name` on GPU `at`, on torch's current stream there."""
+    stream = torch._C._cuda_getCurrentRawStream(at)
+    f = getattr(_lib or lib(), name)
+    if at == torch._C._cuda_getDevice():
+        rc = f(*args, stream)
     else:
-        with torch.cuda.device(dev):
-            rc = getattr(lib(), name)(*args, stream)
-    _check(rc, name)
+        with torch.cuda.device(at):
+            rc = f(*args, stream)
+    if rc != OK:
+        raise SpecDecError(rc, name)
+
+
+def _gpu(t, name):
+    """The index of the GPU that holds t."""
+    at = t.get_device()
+    if at < 0:
+        raise ValueError("%s must be a device tensor" % name)
+    return at
 
 
 def _depth(depth):
@@ -677,20 +701,21 @@ def tree_positions(parent, lens, rows=None, pos=None, status=None):
     """Positions [B, N] of the nodes of trees parent [B, N] whose rows hold lens
     content positions (lens[rows[b]], or lens[b]): length plus depth, -1 for
     nodes that are not used."""
-    _need(parent, "parent", torch.int32)
+    at = _gpu(_need(parent, "parent", _I32), "parent")
     if parent.dim() != 2:
         raise ValueError("parent must be [B, N]")
     B, N = parent.shape
-    dev = parent.device
-    _need(lens, "lens", torch.int32)
-    if lens.dim() != 1 or (rows is None and lens.numel() < B):
+    n = lens.numel()
+    if not _is(lens, _I32, (n,), at) or (rows is None and n < B):
+        _need(lens, "lens", _I32)
+        _on(parent.device, (lens, "lens"))
         raise ValueError("lens must hold one length per row")
-    _on(dev, (lens, "lens"))
     if rows is not None:
-        _ints((B,), dev, (rows, "rows"))
-    pos = _i32((B, N), dev) if pos is None else _out(pos, "pos", B * N, device=dev)
-    _out(status, "status", 1, device=dev)
-    _launch(dev, "specdec_tree_positions", _ptr(parent), B, N, _ptr(lens), _ptr(rows), lens.numel(), _ptr(pos),
+        _ints((B,), parent.device, (rows, "rows"))
+    pos = parent.new_empty((B, N)) if pos is None else _out(pos, "pos", B * N, device=parent.device)
+    if status is not None:
+        _out(status, "status", 1, device=parent.device)
+    _launch(at, "specdec_tree_positions", parent.data_ptr(), B, N, lens.data_ptr(), _ptr(rows), n, pos.data_ptr(),
             _ptr(status))
     return pos
 
@@ -733,9 +758,13 @@ def _heads_view(t, name):
     """A [B, N, heads, Dh] device tensor whose heads are contiguous: its strides."""
     if t.dim() != 4 or t.dtype not in _TORCH_DT or not t.is_cuda:
         raise ValueError("%s must be a [B, N, heads, Dh] float32/float16/bfloat16 device tensor" % name)
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    b, n, h, e = t.stride()
+    if e != 1 and t.shape[3] > 1:
         raise ValueError("%s must have a contiguous last dimension" % name)
-    return (C.c_int64 * 3)(*t.stride()[:3])
+    return _Strides(b, n, h)
+
+
+_Strides = C.c_int64 * 3
 
 
 def rope(x, pos, freq, interleaved=False, factor=1.0, out=None):
@@ -745,21 +774,31 @@ def rope(x, pos, freq, interleaved=False, factor=1.0, out=None):
     in `out`: x itself to work in place, or a new tensor by default, which holds
     no values there.  Returns out."""
     xs = _heads_view(x, "x")
-    B, N, H, Dh = x.shape
-    dev = x.device
-    _ints((B, N), dev, (pos, "pos"))
-    _need(freq, "freq", torch.float64)
-    if freq.dim() != 1:
+    B, N, H, Dh = shape = x.shape
+    at = x.get_device()
+    _ints((B, N), x.device, (pos, "pos"))
+    half = freq.numel()
+    if not _is(freq, torch.float64, (half,), at):
+        _need(freq, "freq", torch.float64)
+        _on(x.device, (freq, "freq"))
         raise ValueError("freq must be one-dimensional")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    elif out.shape != x.shape or out.dtype != x.dtype:
+        out = x.new_empty(shape)
+    elif out.shape != shape or out.dtype != x.dtype:
         raise ValueError("out must have x's shape and type")
-    os_ = _heads_view(out, "out")
-    _on(dev, (freq, "freq"), (out, "out"))
-    _launch(dev, "specdec_rope", _ptr(x), xs, _ptr(out), os_, _TORCH_DT[x.dtype], B, N, H, Dh, _ptr(pos), _ptr(freq),
-            2 * freq.numel(), int(bool(interleaved)), float(factor))
+    elif out.get_device() != at:
+        raise ValueError("out must be on %s" % x.device)
+    _launch(at, "specdec_rope", x.data_ptr(), xs, out.data_ptr(), xs if out is x else _heads_view(out, "out"),
+            _TORCH_DT[x.dtype], B, N, H, Dh, pos.data_ptr(), freq.data_ptr(), 2 * half, 1 if interleaved else 0, float(factor))
     return out
+
+
+def _verified(draft, B, depth, accept_len, next_token, path):
+    """The outputs of a tree's verification: the caller's, or new ones."""
+    dev = draft.device
+    return (draft.new_empty((B,)) if accept_len is None else _out(accept_len, "accept_len", B, device=dev),
+            draft.new_empty((B,)) if next_token is None else _out(next_token, "next_token", B, device=dev),
+            draft.new_empty((B, depth + 1)) if path is None else _out(path, "path", B * (depth + 1), device=dev))
 
 
 def verify_tree_greedy(logits, draft, parent, depth, ws=None, status=None, accept_len=None, next_token=None, path=None,
@@ -772,22 +811,22 @@ def verify_tree_greedy(logits, draft, parent, depth, ws=None, status=None, accep
     N = D + 1
     if N < 1:
         raise ValueError("a tree has one node at least")
-    dev = logits.device
+    at = logits.get_device()
     depth = _depth(depth)
-    _ints((B, N), dev, (draft, "draft"), (parent, "parent"))
-    accept_len = _i32(B, dev) if accept_len is None else _out(accept_len, "accept_len", B, device=dev)
-    next_token = _i32(B, dev) if next_token is None else _out(next_token, "next_token", B, device=dev)
-    path = _i32((B, depth + 1), dev) if path is None else _out(path, "path", B * (depth + 1), device=dev)
-    _out(target_tok, "target_tok", B * N, device=dev)
-    _out(status, "status", 1, device=dev)
+    _ints((B, N), logits.device, (draft, "draft"), (parent, "parent"))
+    accept_len, next_token, path = _verified(draft, B, depth, accept_len, next_token, path)
+    if target_tok is not None:
+        _out(target_tok, "target_tok", B * N, device=logits.device)
+    if status is not None:
+        _out(status, "status", 1, device=logits.device)
     if ws is None:
-        with torch.cuda.device(dev):
-            ws = workspace(B, N - 1, dev)
-    else:
-        _out(ws, "ws", 1, torch.uint8, device=dev)
-    _launch(dev, "specdec_verify_tree_greedy", _ptr(logits), _TORCH_DT[logits.dtype], row_stride, B, N, V, _ptr(draft),
-            _ptr(parent), depth, _ptr(accept_len), _ptr(next_token), _ptr(path), _ptr(target_tok), _ptr(ws), ws.numel(),
-            _ptr(status))
+        with torch.cuda.device(at):
+            ws = workspace(B, N - 1, logits.device)
+    elif ws.dtype is not torch.uint8 or ws.get_device() != at or not ws.is_contiguous():
+        _out(ws, "ws", 1, torch.uint8, device=logits.device)
+    _launch(at, "specdec_verify_tree_greedy", logits.data_ptr(), _TORCH_DT[logits.dtype], row_stride, B, N, V,
+            draft.data_ptr(), parent.data_ptr(), depth, accept_len.data_ptr(), next_token.data_ptr(), path.data_ptr(),
+            _ptr(target_tok), ws.data_ptr(), ws.numel(), _ptr(status))
     return accept_len, next_token, path
 
 
@@ -797,30 +836,28 @@ def verify_tree_sample(p, draft, parent, u_accept, u_draw, depth, ws=None, statu
     [B, N, V] (float32) and uniforms u_accept, u_draw [B, N], at most `depth`
     accepted.  The workspace is sample_verify_workspace(B, N - 1, V).  Returns
     (accept_len [B], next_token [B], path [B, depth+1])."""
-    _need(p, "p", torch.float32)
+    at = _gpu(_need(p, "p", torch.float32), "p")
     if p.dim() != 3 or p.shape[1] < 1:
         raise ValueError("p must be [B, N, V]")
     B, N, V = p.shape
-    dev = p.device
     depth = _depth(depth)
-    _ints((B, N), dev, (draft, "draft"), (parent, "parent"))
+    _ints((B, N), p.device, (draft, "draft"), (parent, "parent"))
     for t, n in ((u_accept, "u_accept"), (u_draw, "u_draw")):
-        _need(t, n, torch.float32)
-        if tuple(t.shape) != (B, N):
+        if not _is(t, torch.float32, (B, N), at):
+            _need(t, n, torch.float32)
+            _on(p.device, (t, n))
             raise ValueError("%s must be [B, N]" % n)
-        _on(dev, (t, n))
-    accept_len = _i32(B, dev) if accept_len is None else _out(accept_len, "accept_len", B, device=dev)
-    next_token = _i32(B, dev) if next_token is None else _out(next_token, "next_token", B, device=dev)
-    path = _i32((B, depth + 1), dev) if path is None else _out(path, "path", B * (depth + 1), device=dev)
-    _out(status, "status", 1, device=dev)
+    accept_len, next_token, path = _verified(draft, B, depth, accept_len, next_token, path)
+    if status is not None:
+        _out(status, "status", 1, device=p.device)
     if ws is None and B > 0:
-        with torch.cuda.device(dev):
-            ws = sample_verify_workspace(B, N - 1, V, dev)
-    elif ws is not None:
-        _out(ws, "ws", 1, torch.uint8, device=dev)
-    _launch(dev, "specdec_verify_tree_sample", _ptr(p), B, N, V, _ptr(draft), _ptr(parent), _ptr(u_accept), _ptr(u_draw),
-            depth, _ptr(accept_len), _ptr(next_token), _ptr(path), _ptr(ws), 0 if ws is None else ws.numel(),
-            _ptr(status))
+        with torch.cuda.device(at):
+            ws = sample_verify_workspace(B, N - 1, V, p.device)
+    elif ws is not None and (ws.dtype is not torch.uint8 or ws.get_device() != at or not ws.is_contiguous()):
+        _out(ws, "ws", 1, torch.uint8, device=p.device)
+    _launch(at, "specdec_verify_tree_sample", p.data_ptr(), B, N, V, draft.data_ptr(), parent.data_ptr(),
+            u_accept.data_ptr(), u_draw.data_ptr(), depth, accept_len.data_ptr(), next_token.data_ptr(), path.data_ptr(),
+            _ptr(ws), 0 if ws is None else ws.numel(), _ptr(status))
     return accept_len, next_token, path
 
 
@@ -829,30 +866,32 @@ def tree_compact(kv_new, draft, path, accept_len, kv_path=None, draft_path=None,
     kv_new [L, 2, B, H, N, Dh], draft [B, N], path [B, depth+1] and accept_len [B]
     give (kv_path [L, 2, B, H, depth+1, Dh], draft_path [B, depth]), which the
     appends and realignments take.  Entries past accept_len are not written."""
-    _need(kv_new, "kv_new")
     if kv_new.dim() != 6 or kv_new.shape[1] != 2 or kv_new.dtype not in _TORCH_DT:
         raise ValueError("kv_new must be a [L, 2, B, H, N, Dh] float32/float16/bfloat16 tensor")
+    at = _gpu(_need(kv_new, "kv_new"), "kv_new")
     L, _, B, H, N, Dh = kv_new.shape
-    dev = kv_new.device
-    _need(path, "path", torch.int32)
-    if path.dim() != 2 or path.shape[0] != B or path.shape[1] < 1:
+    if path.dim() != 2 or path.shape[1] < 1:
         raise ValueError("path must be [B, depth+1]")
     depth = _depth(path.shape[1] - 1)
+    dev = kv_new.device
+    _ints((B, depth + 1), dev, (path, "path"))
     _ints((B, N), dev, (draft, "draft"))
     _ints((B,), dev, (accept_len, "accept_len"))
-    _on(dev, (path, "path"))
     shape = (L, 2, B, H, depth + 1, Dh)
     if kv_path is None:
-        kv_path = torch.empty(shape, dtype=kv_new.dtype, device=dev)
-    else:
+        kv_path = kv_new.new_empty(shape)
+    elif not _is(kv_path, kv_new.dtype, shape, at):
         _need(kv_path, "kv_path", kv_new.dtype)
-        if tuple(kv_path.shape) != shape:
-            raise ValueError("kv_path must be [L, 2, B, H, depth+1, Dh]")
         _on(dev, (kv_path, "kv_path"))
-    draft_path = _i32((B, depth), dev) if draft_path is None else _out(draft_path, "draft_path", B * depth, device=dev)
-    _out(status, "status", 1, device=dev)
-    _launch(dev, "specdec_tree_compact", _ptr(kv_new), _TORCH_DT[kv_new.dtype], L, B, H, N, Dh, _ptr(draft), _ptr(path),
-            _ptr(accept_len), depth, _ptr(kv_path), _ptr(draft_path), _ptr(status))
+        raise ValueError("kv_path must be [L, 2, B, H, depth+1, Dh]")
+    if draft_path is None:
+        draft_path = draft.new_empty((B, depth))
+    elif not _is(draft_path, _I32, (B, depth), at):
+        _out(draft_path, "draft_path", B * depth, device=dev)
+    if status is not None:
+        _out(status, "status", 1, device=dev)
+    _launch(at, "specdec_tree_compact", kv_new.data_ptr(), _TORCH_DT[kv_new.dtype], L, B, H, N, Dh, draft.data_ptr(),
+            path.data_ptr(), accept_len.data_ptr(), depth, kv_path.data_ptr(), draft_path.data_ptr(), _ptr(status))
     return kv_path, draft_path
 
 
@@ -882,39 +921,46 @@ def tree_attention(q, cache, layer, kv_new, parent, rows=None, group=0, scale=No
     scale defaults to Dh**-0.5.  Nodes outside the tree are left as they are in
     `out` (a new tensor by default, which holds no values there).  Returns out."""
     qs = _heads_view(q, "q")
-    B, N, Hq, Dh = q.shape
-    dev = q.device
+    B, N, Hq, Dh = shape = q.shape
+    at, dt = q.get_device(), q.dtype
     paged = isinstance(cache, PagedKV)
     if not paged and not isinstance(cache, SeqBuf):
         raise ValueError("cache must be a PagedKV or a SeqBuf")
     kv = cache.pages if paged else cache.kv
-    L, H = kv.shape[0], kv.shape[3]
-    if kv.shape[5] != Dh or q.dtype != kv.dtype:
+    L, _, _, H, _, kv_dh = kv.shape
+    if kv_dh != Dh or dt != kv.dtype:
         raise ValueError("q must have the cache's head size and type")
-    _need(kv_new, "kv_new", kv.dtype)
-    if tuple(kv_new.shape) != (L, 2, B, H, N, Dh):
+    if kv.get_device() != at:
+        raise ValueError("cache must be on %s" % q.device)
+    if not _is(kv_new, dt, (L, 2, B, H, N, Dh), at):
+        _need(kv_new, "kv_new", dt)
+        _on(q.device, (kv_new, "kv_new"))
         raise ValueError("kv_new must be [L, 2, B, H, N, Dh] of the cache's geometry")
-    _ints((B, N), dev, (parent, "parent"))
+    _ints((B, N), q.device, (parent, "parent"))
     if rows is not None:
-        _ints((B,), dev, (rows, "rows"))
+        _ints((B,), q.device, (rows, "rows"))
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    elif out.shape != q.shape or out.dtype != q.dtype:
+        out = q.new_empty(shape)
+    elif out.shape != shape or out.dtype != dt:
         raise ValueError("out must have q's shape and type")
-    os_ = _heads_view(out, "out")
-    _on(dev, (kv, "cache"), (kv_new, "kv_new"), (out, "out"))
-    group = int(group)
-    if not paged and group > 0 and cache.width is not None and cache.width.numel() * group < B:
-        raise ValueError("the rectangle's width tensor needs one entry per group")
-    _out(status, "status", 1, device=dev)
+    elif out.get_device() != at:
+        raise ValueError("out must be on %s" % q.device)
+    if status is not None:
+        _out(status, "status", 1, device=q.device)
     if ws is None:
         if B == 0:
             return out
-        ws = tree_attention_workspace(B, N, Hq, H, Dh, dev)
+        ws = tree_attention_workspace(B, N, Hq, H, Dh, q.device)
+    elif ws.dtype is not torch.uint8 or ws.get_device() != at or not ws.is_contiguous():
+        _out(ws, "ws", 1, torch.uint8, device=q.device)
+    rest = (int(layer), q.data_ptr(), qs, Hq, kv_new.data_ptr(), parent.data_ptr(), B, N,
+            Dh ** -0.5 if scale is None else float(scale), out.data_ptr(), _heads_view(out, "out"), ws.data_ptr(), ws.numel(),
+            _ptr(status))
+    if paged:
+        _launch(at, "specdec_tree_attention_paged", C.byref(cache.c), _ptr(rows), *rest)
     else:
-        _out(ws, "ws", 1, torch.uint8, device=dev)
-    scale = Dh ** -0.5 if scale is None else float(scale)
-    head = (C.byref(cache.c), _ptr(rows)) if paged else (C.byref(cache.c), _ptr(rows), group)
-    _launch(dev, "specdec_tree_attention_paged" if paged else "specdec_tree_attention", *head, int(layer), _ptr(q), qs, Hq,
-            _ptr(kv_new), _ptr(parent), B, N, scale, _ptr(out), os_, _ptr(ws), ws.numel(), _ptr(status))
+        group = int(group)
+        if group > 0 and cache.width is not None and cache.width.numel() * group < B:
+            raise ValueError("the rectangle's width tensor needs one entry per group")
+        _launch(at, "specdec_tree_attention", C.byref(cache.c), _ptr(rows), group, *rest)
     return out

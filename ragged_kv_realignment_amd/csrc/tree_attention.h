@@ -96,11 +96,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// The largest of eight scores, NaN passed over.  (The median with +inf is the
-// larger of two; fmaxf would first canonicalise each operand.)
+// The largest of eight scores; NaN, whose query's result is NaN in any case, stays.
+// (fmaxf, which passes NaN over, would first canonicalise each operand.)
 __device__ __forceinline__ float max8(f32x4 a, f32x4 b) {
-  auto larger = [](float x, float y) { return __builtin_amdgcn_fmed3f(x, y, INFINITY); };
-  return larger(larger(larger(a[0], a[1]), larger(a[2], a[3])), larger(larger(b[0], b[1]), larger(b[2], b[3])));
+  auto larger = [](float x, float y) { return __builtin_elementwise_maximum(x, y); };
+  return larger(larger(larger(larger(a[0], a[1]), a[2]), larger(larger(a[3], b[0]), b[1])), larger(b[2], b[3]));
 }
 
 template <int DT>

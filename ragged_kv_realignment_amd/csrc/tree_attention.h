@@ -959,12 +959,14 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
       where(at);
       weights(s, w);
       __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(1);
       read_v(x, tile_at(i), at, page);
       products(x, s, w);
       fetch(i + U + 1, page);
       __builtin_amdgcn_sched_barrier(0);  // V's registers are free before K's fill
       read_k(x, tile_at(i + 1));
       scores(x, s);
+      __builtin_amdgcn_s_setprio(0);
       raise(s);
     }
     for (; i < steps; ++i) {

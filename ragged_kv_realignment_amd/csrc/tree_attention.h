@@ -189,8 +189,7 @@ namespace {
 // Ancestor bits of every node (itself included) from its raw parent, a node per
 // thread, by pointer doubling in LDS: after round k a node holds the bits of 2^k
 // generations and the pointer past them.  A node outside the tree gets none.
-__device__ __forceinline__ void tree_ancestors(int N, int raw, int32_t *status, int *ptr,
-                                               uint32_t (*anc)[kMaxNodes / 32]) {
+__device__ __forceinline__ void tree_parents(int N, int raw, int32_t *status, int *ptr, uint32_t (*anc)[kMaxNodes / 32]) {
   const int t = threadIdx.x, words = (N + 31) / 32;
   bool bad = false;
   if (t < N) {
@@ -198,6 +197,9 @@ __device__ __forceinline__ void tree_ancestors(int N, int raw, int32_t *status, 
     for (int k = 0; k < words; ++k) anc[t][k] = (t >> 5) == k ? 1u << (t & 31) : 0u;
   }
   if (bad) set_status(status, SPECDEC_S_TREE);
+}
+__device__ __forceinline__ void tree_ancestors(int N, int *ptr, uint32_t (*anc)[kMaxNodes / 32]) {
+  const int t = threadIdx.x, words = (N + 31) / 32;
   for (int span = 1; span < N; span <<= 1) {
     __syncthreads();
     int q = 0;
@@ -221,11 +223,12 @@ __device__ __forceinline__ void tree_ancestors(int N, int raw, int32_t *status, 
   __syncthreads();
 }
 
-// Loads that write LDS directly: lane i's 16 bytes go to `to` (the same in all
-// lanes) + 16 i.
-__device__ __forceinline__ void load_lds(const void *from, void *to) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                   (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+// Loads that write LDS directly: lane i's 16 bytes go to byte `to` (the same in all
+// lanes) of LDS + 16 i.  They have no output register; wait_loads() waits for them.
+// (The compiler, which would know the builtin's write to LDS, has every read of LDS
+// wait for all of them, the next tiles' too.)
+__device__ __forceinline__ void load_lds(const void *from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
@@ -238,67 +241,9 @@ __device__ __forceinline__ void wait_loads() {
 }
 __device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Reads of LDS that those loads have written, waited for here.  As ordinary
-// loads the compiler would have each of them wait for every load to LDS that is
-// out, the next tiles' too.
-template <int OFF>
-__device__ __forceinline__ void lds_read(u32x4 &a, u32x4 &b, u32x4 &c, u32x4 &d, uint32_t p, uint32_t q) {
-  asm volatile(
-      "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %4 offset:%6\n\tds_read_b128 %3, %5 offset:%6\n\t"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
-      : "v"(p), "v"(q), "n"(OFF)
-      : "memory");
-}
-template <int OFF>
-__device__ __forceinline__ void lds_read(u32x4 &a, u32x4 &b, u32x4 &c, u32x4 &d, u32x4 &e, u32x4 &f, u32x4 &g, u32x4 &h,
-                                         uint32_t p, uint32_t q, uint32_t r, uint32_t s) {
-  asm volatile(
-      "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %10\n\tds_read_b128 %3, %11\n\t"
-      "ds_read_b128 %4, %8 offset:%12\n\tds_read_b128 %5, %9 offset:%12\n\tds_read_b128 %6, %10 offset:%12\n\t"
-      "ds_read_b128 %7, %11 offset:%12\n\ts_waitcnt lgkmcnt(0)"
-      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h)
-      : "v"(p), "v"(q), "v"(r), "v"(s), "n"(OFF)
-      : "memory");
-}
-// The rows at q, r and s lie ROW, 2 ROW and 3 ROW bytes on; and two words.
-template <int OFF, int ROW>
-__device__ __forceinline__ void lds_read(u32x4 &a, u32x4 &b, u32x4 &c, u32x4 &d, u32x4 &e, u32x4 &f, u32x4 &g, u32x4 &h,
-                                         uint32_t &y, uint32_t &z, uint32_t p, uint32_t q, uint32_t r, uint32_t s,
-                                         uint32_t at_y, uint32_t at_z) {
-  asm volatile(
-      "ds_read_b128 %0, %10\n\tds_read_b128 %1, %11 offset:%16\n\tds_read_b128 %2, %12 offset:%17\n\t"
-      "ds_read_b128 %3, %13 offset:%18\n\tds_read_b128 %4, %10 offset:%19\n\tds_read_b128 %5, %11 offset:%20\n\t"
-      "ds_read_b128 %6, %12 offset:%21\n\tds_read_b128 %7, %13 offset:%22\n\tds_read_b32 %8, %14\n\tds_read_b32 %9, %15\n\t"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h), "=&v"(y), "=&v"(z)
-      : "v"(p), "v"(q), "v"(r), "v"(s), "v"(at_y), "v"(at_z), "n"(ROW), "n"(2 * ROW), "n"(3 * ROW), "n"(OFF), "n"(OFF + ROW),
-        "n"(OFF + 2 * ROW), "n"(OFF + 3 * ROW)
-      : "memory");
-}
-template <int OFF, int ROW>
-__device__ __forceinline__ void lds_read(u32x2 &a, u32x2 &b, u32x2 &c, u32x2 &d, u32x2 &e, u32x2 &f, u32x2 &g, u32x2 &h,
-                                         uint32_t &y, uint32_t &z, uint32_t p, uint32_t q, uint32_t r, uint32_t s,
-                                         uint32_t at_y, uint32_t at_z) {
-  asm volatile(
-      "ds_read_b64 %0, %10\n\tds_read_b64 %1, %11 offset:%16\n\tds_read_b64 %2, %12 offset:%17\n\t"
-      "ds_read_b64 %3, %13 offset:%18\n\tds_read_b64 %4, %10 offset:%19\n\tds_read_b64 %5, %11 offset:%20\n\t"
-      "ds_read_b64 %6, %12 offset:%21\n\tds_read_b64 %7, %13 offset:%22\n\tds_read_b32 %8, %14\n\tds_read_b32 %9, %15\n\t"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h), "=&v"(y), "=&v"(z)
-      : "v"(p), "v"(q), "v"(r), "v"(s), "v"(at_y), "v"(at_z), "n"(ROW), "n"(2 * ROW), "n"(3 * ROW), "n"(OFF), "n"(OFF + ROW),
-        "n"(OFF + 2 * ROW), "n"(OFF + 3 * ROW)
-      : "memory");
-}
-
-// Words of LDS, beside loads to LDS that are out.
-__device__ __forceinline__ uint32_t lds_get(uint32_t at) {
-  uint32_t v;
-  asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ void lds_set(uint32_t at, uint32_t v) {
-  asm volatile("ds_write_b32 %0, %1" ::"v"(at), "v"(v) : "memory");
+template <class T>
+__device__ __forceinline__ T lds_read(uint32_t at) {
+  return *(const __attribute__((address_space(3))) T *)(uintptr_t)at;
 }
 
 // How the pieces of a row of P are turned among its slots in LDS (256 bytes are
@@ -461,7 +406,7 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
   constexpr int KEY_BYTES = SHARED ? ST * KW * TILE_BYTES : 0;
   constexpr int O_BYTES = KW > 1 ? NW * RT * 16 * LROW * 4 : 0;
 
-  __shared__ int s_page[SHARED && PAGED ? kWindow : 1];
+  __shared__ uint32_t s_page[SHARED && PAGED ? kWindow : 1];
   __shared__ __align__(1024) char s_mem[KEY_BYTES > O_BYTES ? KEY_BYTES : O_BYTES > 0 ? O_BYTES : 16];
   __shared__ uint32_t s_anc[kMaxNodes][kMaxNodes / 32];
   __shared__ int s_ptr[kMaxNodes], s_last, s_odd, s_hole;
@@ -728,7 +673,10 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
       load_k(x0, tl, rho);
       load_v(x0, tl, rho);
     }
-    if (need_anc) tree_ancestors(N, raw_parent, p.status, s_ptr, s_anc);
+    if (need_anc) {
+      tree_parents(N, raw_parent, p.status, s_ptr, s_anc);
+      tree_ancestors(N, s_ptr, s_anc);
+    }
     settle<DT>(q, p.negate);
     uint32_t vm = (uint32_t)__ballot(valid);  // keys of the tile that exist
     auto step = [&](auto plain) {
@@ -782,7 +730,7 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
     // looked up tile by tile they would return in order with the keys that are on
     // their way.
     int window = 0, filled = 0;  // its first block; the first tile that is not all in it
-    const uint32_t lds0 = lds_offset(s_mem) + kw * TILE_BYTES, hole_at = lds_offset(&s_hole);
+    const uint32_t lds0 = lds_offset(s_mem) + kw * TILE_BYTES;
     // The page ids of tiles i0 .. i1 are in the window.  Every wave of the
     // workgroup comes here, past a barrier: the window moves for all together.
     auto need_pages = [&](int i0, int i1) {
@@ -793,11 +741,8 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
       for (int i = t; i < n; i += NT) {
         const int page = table[window + i];
         const bool in = (uint32_t)page < (uint32_t)p.n_pages;
-        if (!in) {
-          bad_page = true;
-          lds_set(hole_at, 1u);
-        }
-        lds_set(lds_offset(&s_page[i]), ((in ? (uint32_t)page : 0u) * H + h) * p.page);
+        if (!in) bad_page = s_hole = true;
+        s_page[i] = ((in ? (uint32_t)page : 0u) * H + h) * p.page;
       }
       filled = window + n == blocks ? cache_tiles : (window + n) * p.page / kTile;
       barrier();
@@ -815,21 +760,18 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
       blk[j] = PAGED ? (int)fdiv((uint32_t)pos[j], p.page_div) : 0;
       slot[j] = pos[j] - blk[j] * p.page;
     }
-    // the words of LDS that begin those rows' blocks
-    auto where = [&](uint32_t (&at)[2]) {
+    // the rows of the blocks that those lie in
+    auto pages = [&](uint32_t (&at)[PASS]) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int y = min(j, PASS - 1);
-        at[j] = lds_offset(s_page) + (PAGED ? (uint32_t)max((pos[y] < len ? blk[y] : end_block) - window, 0) * 4u : 0u);
-      }
+      for (int j = 0; j < PASS; ++j) at[j] = PAGED ? s_page[max((pos[j] < len ? blk[j] : end_block) - window, 0)] : 0u;
     };
-    // the loads of tile i, with those words
-    auto fetch = [&](int i, const uint32_t (&page)[2]) {
+    // the loads of tile i, with those
+    auto fetch = [&](int i, const uint32_t (&page)[PASS]) {
       const int tl = tile_of(i);
       const bool is_old = tl < cache_tiles;
       const char *kb = static_cast<const char *>(is_old ? p.k_old : p.k_new);
       const char *vb = static_cast<const char *>(is_old ? p.v_old : p.v_new);
-      char *to = s_mem + ((i % ST) * KW + kw) * TILE_BYTES + rw * (kWave * 16);
+      const uint32_t to = lds0 + (uint32_t)((i % ST) * KW * TILE_BYTES + rw * (kWave * 16));
 #pragma unroll
       for (int j = 0; j < PASS; ++j) {
         const int row = (in_group + j * RW * kWave) / P;
@@ -860,63 +802,51 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
     const uint32_t k_at = (uint32_t)(c * P * 16 + ((g ^ swz<P>(c)) << 4));
     const uint32_t v_at = (uint32_t)((kTile + g * 4) * P * 16 + (((c * NE * ES >> 4) ^ swz<P>(g * 4)) << 4) + c * NE * ES % 16);
     auto read_k = [&](Keys &x, uint32_t tile) {
-      const uint32_t a = tile + k_at;
-      if constexpr (KS == 2) {
-        lds_read<HALF>(x.k[0][0], x.k[0][1], x.k[1][0], x.k[1][1], a, a ^ 64u);
-      } else {
 #pragma unroll
-        for (int s = 0; s < KS; s += 4)
-          lds_read<HALF>(x.k[0][s], x.k[0][s + 1], x.k[0][s + 2], x.k[0][s + 3], x.k[1][s], x.k[1][s + 1],
-                         x.k[1][s + 2], x.k[1][s + 3], a ^ (64u * s), a ^ (64u * (s + 1)), a ^ (64u * (s + 2)),
-                         a ^ (64u * (s + 3)));
+      for (int s = 0; s < KS; ++s) {
+        const uint32_t a = tile + (k_at ^ (64u * s));
+        x.k[0][s] = lds_read<u32x4>(a);
+        x.k[1][s] = lds_read<u32x4>(a + HALF);
       }
     };
-    auto read_v = [&](Keys &x, uint32_t tile, const uint32_t (&at)[2], uint32_t (&page)[2]) {
-      const uint32_t a = tile + v_at;
-      // row g * 4 + i: its turn is (g * 4 + i) & 15, or of two rows of 8 pieces (g * 2 + i / 2) & 7
-      constexpr uint32_t T1 = P == 8 ? 0u : 16u, T2 = P == 8 ? 16u : 32u, T3 = P == 8 ? 16u : 48u;
-      constexpr int N_D = VD < 4 ? 1 : VD / 4;
+    auto read_v = [&](Keys &x, uint32_t tile) {
 #pragma unroll
-      for (int d = 0; d < N_D; ++d) {
-        const uint32_t e = a ^ (16u * d);
-        if constexpr (VD == 2) {
-          u32x2 y[8];
-          lds_read<HALF, P * 16>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], page[0], page[1], e, e ^ T1, e ^ T2, e ^ T3, at[0],
-                                 at[1]);
+      for (int i = 0; i < 4; ++i) {
+        // row g * 4 + i: its turn is (g * 4 + i) & 15, or of two rows of 8 pieces (g * 2 + i / 2) & 7
+        const uint32_t turn = (uint32_t)(P == 8 ? i >> 1 : i) * 16u;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x.v[i][0] = y[i][0];
-            x.v[i][1] = y[i][1];
+        for (int d = 0; d < (VD < 4 ? 1 : VD / 4); ++d)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t a = tile + ((v_at ^ turn ^ (16u * d)) + i * P * 16 + y * HALF);
+            if constexpr (VD == 2) {
+              const u32x2 w = lds_read<u32x2>(a);
+              x.v[y * 4 + i][0] = w[0];
+              x.v[y * 4 + i][1] = w[1];
+            } else {
+              const u32x4 w = lds_read<u32x4>(a);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) x.v[y * 4 + i][d * 4 + z] = w[z];
+            }
           }
-        } else {
-          u32x4 y[8];
-          lds_read<HALF, P * 16>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], page[0], page[1], e, e ^ T1, e ^ T2, e ^ T3, at[0],
-                                 at[1]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int z = 0; z < 4; ++z) x.v[i][d * 4 + z] = y[i][z];
-        }
       }
     };
     if constexpr (PAD) {  // pieces past Dh are never written: they read as zeros
       for (int i = t; i < ST * KW * TILE_BYTES / 16; i += NT) reinterpret_cast<u32x4 *>(s_mem)[i] = (u32x4)(0u);
     }
+    load_q();
     __syncthreads();  // s_hole, and the zeros
     need_pages(0, U);
+    // the last waits for other loads: the keys on their way would be waited for too
+    if (need_anc) tree_parents(N, raw_parent, p.status, s_ptr, s_anc);
+    settle<DT>(q, p.negate);
 #pragma unroll 1
     for (int i = 0; i <= U; ++i) {
-      uint32_t at[2], page[2] = {0u, 0u};
-      where(at);
-      if constexpr (PAGED) {
-        page[0] = lds_get(at[0]);
-        page[1] = lds_get(at[1]);
-      }
+      uint32_t page[PASS];
+      pages(page);
       fetch(i, page);
     }
-    load_q();
-    if (need_anc) tree_ancestors(N, raw_parent, p.status, s_ptr, s_anc);
-    settle<DT>(q, p.negate);
+    if (need_anc) tree_ancestors(N, s_ptr, s_anc);
     // keys of a tile that exist: all but the last ones, unless some page was bad
     auto existing_keys = [&](int tl, bool hole) -> uint32_t {
       const int n = tl < cache_tiles ? len - tl * kTile : N - (tl - cache_tiles) * kTile;
@@ -929,14 +859,19 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
       return vm;
     };
     Scores s;
+    Keys x;
     auto tile_at = [&](int i) { return lds0 + (uint32_t)((i % ST) * KW * TILE_BYTES); };
-    auto new_scores = [&](int i, bool hole) {
+    // of tile i, all but its weights
+    auto begin = [&](int i, bool hole) {
       const int tl = tile_of(i);
-      Keys x;
       read_k(x, tile_at(i));
       scores(x, s);
+      read_v(x, tile_at(i));
       const uint32_t vm = existing_keys(tl, hole);
-      if (tl >= cache_tiles || vm != 0xFFFFFFFFu) mask_scores(s, tl, vm);
+      if (tl >= cache_tiles || vm != 0xFFFFFFFFu) {
+        mask_scores(s, tl, vm);
+        mask_values(x, tl, vm);
+      }
       raise(s);
     };
     bool hole = false;
@@ -945,45 +880,46 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
       due += U;
       wait_loads<0>();  // this wave's share of the tiles up to i + U
       barrier();        // the others', and all are past the tiles before i
-      hole = uniform((int)lds_get(hole_at)) != 0;
+      hole = uniform(s_hole) != 0;
       need_pages(i + U + 1, i + 2 * U);
     };
     meet();
-    if (mine > 0) new_scores(0, hole);
+    if (mine > 0) begin(0, hole);
+    // A step reads the next tile's K while V is multiplied, and its V beside the
+    // softmax, where there are registers for both.
+    constexpr bool AHEAD = DHP * ES <= 256;
     for (; tile_of(i + 1) < whole_tiles; ++i) {  // whole tiles, and one after them
       if (i == due) meet();
-      if (hole) break;
-      Keys x;
+      if (PAGED && hole) break;
       u32x4 w[RT];
-      uint32_t at[2], page[2];
-      where(at);
+      uint32_t page[PASS];
+      pages(page);
       weights(s, w);
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_setprio(1);
-      read_v(x, tile_at(i), at, page);
+      if constexpr (AHEAD) read_k(x, tile_at(i + 1));
+      __builtin_amdgcn_sched_barrier(0);
       products(x, s, w);
       fetch(i + U + 1, page);
       __builtin_amdgcn_sched_barrier(0);  // V's registers are free before K's fill
-      read_k(x, tile_at(i + 1));
+      if constexpr (!AHEAD) read_k(x, tile_at(i + 1));
       scores(x, s);
       __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+      read_v(x, tile_at(i + 1));
+      __builtin_amdgcn_sched_barrier(0);
       raise(s);
     }
     for (; i < steps; ++i) {
       if (i == due) meet();
       if (i >= mine) continue;
-      Keys x;
       u32x4 w[RT];
-      uint32_t at[2], page[2];
-      where(at);
+      uint32_t page[PASS];
+      pages(page);
       weights(s, w);
-      read_v(x, tile_at(i), at, page);
       fetch(i + U + 1, page);
-      const int tl = tile_of(i);
-      const uint32_t vm = existing_keys(tl, hole);
-      if (tl >= cache_tiles || vm != 0xFFFFFFFFu) mask_values(x, tl, vm);
       products(x, s, w);
-      if (i + 1 < mine) new_scores(i + 1, hole);
+      if (i + 1 < mine) begin(i + 1, hole);
     }
     __syncthreads();  // the keys' LDS is free
   }
@@ -1098,7 +1034,10 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
   }
   __syncthreads();
   if (!s_last) return;
-  if (!need_anc) tree_ancestors(N, t < N ? p.parent[(size_t)b * N + t] : 0, p.status, s_ptr, s_anc);
+  if (!need_anc) {
+    tree_parents(N, t < N ? p.parent[(size_t)b * N + t] : 0, p.status, s_ptr, s_anc);
+    tree_ancestors(N, s_ptr, s_anc);
+  }
   constexpr int PIECES = DHP / 8, NB = 4;  // parts whose loads are in flight together
   const int most = min(ROWS, M - rb * ROWS);
   for (int i = t; i < most * PIECES; i += NT) {

@@ -799,29 +799,52 @@ EXPORT int specdec_tree_compact(const void *kv_new, int dtype, int layers, int B
 }
 
 // Query tiles by the number of query rows M = N * Hq / Hkv of a KV head: few
-// rows leave all four waves to the keys; more rows go to more tiles per wave,
-// then to more waves, which leave fewer for the keys.
+// rows leave all four waves to the keys, which go straight to registers (rw 1);
+// more rows share the keys through LDS.  Microseconds of a call with 16 sequences
+// of 256 to 2048 positions and 8 KV heads, and of one with 2 of 40001 to 65537
+// and 2, pages of 16, for (rt,rw,kw):
+//   bf16, Dh 128     (1,1,4)    (2,1,4)    (1,4,2)    (1,6,2)    (1,8,1)    (2,8,1)
+//     M = 16         22 / 33    23 / 33    29 / 42    30 / 45    31 / 46    39 / 55
+//     M = 32         25 / 49    25 / 44    29 / 43    31 / 46    32 / 47    39 / 55
+//     M = 64         48 / 67    28 / 58    30 / 45    32 / 48    33 / 48    41 / 57
+//     M = 96         66 / 77    34 / 70    58 / 55    34 / 49    35 / 50    42 / 59
+//     M = 128        75 / 88    57 / 87    59 / 56    66 / 61    37 / 52    44 / 60
+//     M = 160       110 / 99    69 / 92    79 / 67    69 / 62    80 / 67    47 / 62
+//     M = 256      152 / 147   83 / 102    85 / 82    89 / 74    81 / 68    53 / 67
+//   fp32, Dh 64
+//     M = 32         30 / 50    33 / 41    44 / 61    57 / 75    67 / 89   115 / 146
+//     M = 64         64 / 76    44 / 61    45 / 61    58 / 76    68 / 90   115 / 146
+//     M = 96         82 / 90    60 / 77   102 / 89    60 / 77    69 / 90   116 / 147
+//     M = 128       98 / 104   100 / 97   103 / 90   138 / 118   70 / 92   117 / 148
+//     M = 256      194 / 186  159 / 167  163 / 156  198 / 164  180 / 148  127 / 152
+//   a wave of one tile  (1,1,4), (1,8,1) at Dh 256 of bf16, at Dh 128 of fp32
+//     M = 16         35 / 56    54 / 73        42 / 56   122 / 155
+//     M = 32         68 / 90    55 / 75        94 / 92   124 / 156
+//     M = 48         93 / 98    57 / 77       133 / 124  124 / 157
+//     M = 64       101 / 117    59 / 79       144 / 153  125 / 158
+//     M = 128      200 / 204    66 / 84       286 / 294  130 / 161
 namespace sd {
 AttnShape attn_shape(int dtype, int Dh, int M) {
   AttnShape a;
   a.dhp = Dh <= 64 ? 64 : Dh <= 128 ? 128 : 256;
   const int most = attn_most_tiles(dtype, a.dhp);
-  if (M <= 16 * most || !attn_shared(dtype, a.dhp)) {
+  const int direct = most == 2 ? 32 : dtype == SPECDEC_F32 ? 48 : 16;
+  if (M <= direct || !attn_shared(dtype, a.dhp)) {
     a.rt = M <= 16 || most == 1 ? 1 : 2;
     a.rw = 1;
     a.kw = 4;
     return a;
   }
-  a.kw = 1;
   a.rt = 1;
   if (M <= 64 && attn_share_keys(dtype, a.dhp) == 2) {
     a.rw = 4;
     a.kw = 2;
-  } else if (most == 2 && (M <= 96 || (M > 128 && M <= 192))) {
-    a.rw = 6;  // blocks of 96 rows: the least rows left over
+  } else if (M <= 96 && most == 2) {
+    a.rw = 6;
     a.kw = 2;
   } else {
     a.rw = 8;
+    a.kw = 1;
     a.rt = most == 2 && M > 128 ? 2 : 1;
   }
   return a;

@@ -62,6 +62,7 @@ constexpr int kTile = 32;        // keys of a wave's step
 constexpr float kSlack = 8.0f;   // log2 of the largest weight before the maximum is raised
 constexpr int kWindow = 1024;       // page ids in LDS
 constexpr int kMinUnits = 4;      // of a part (see plan)
+constexpr int kJoin = 16;           // parts that one workgroup adds at once
 constexpr float kLow = -1e30f;   // running maximum before the first key
 
 template <int DT> constexpr int es() { return DT == 0 ? 4 : 2; }
@@ -1023,50 +1024,75 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
   }
   if (SHARED || k.slot < 0) return;
 
-  // One of several workgroups of the segment: the last to arrive adds them.
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  if (t == 0) {
-    unsigned int *count = p.counters + (size_t)k.slot0 * kCountStride;
-    const bool last = atomicAdd(count, 1u) == (unsigned)(k.parts - 1);
-    if (last) store_agent(count, 0u);
-    s_last = last;
+  // One of several workgroups of the segment: the last to arrive adds them.  Of
+  // more than kJoin parts, first the last of each kJoin in turn adds those into the
+  // first one's slot, then the last of these adds the sums: 130 parts of 16 rows by
+  // one workgroup alone took 30 us.
+  constexpr int PIECES = DHP / 8, NB = 4;  // parts whose loads are in flight together
+  const int most = min(ROWS, M - rb * ROWS);
+  // Whether this is the last of n workgroups; what it stored before is there then.
+  auto last_of = [&](int n, int line) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (t == 0) {
+      unsigned int *count = p.counters + (size_t)line * kCountStride;
+      const bool last = atomicAdd(count, 1u) == (unsigned)(n - 1);
+      if (last) store_agent(count, 0u);
+      s_last = last;
+    }
+    __syncthreads();
+    return s_last != 0;
+  };
+  // Slots from, from + step, ...: n of them, to the output or to the first.  (The
+  // pieces of a row are of one wave, which has read them all when it writes.)
+  static_assert(kWave % PIECES == 0, "a row's pieces in one wave");
+  auto join = [&](int from, int step, int n, bool final) {
+    for (int i = t; i < most * PIECES; i += NT) {
+      const int e = i % PIECES * 8, brow = i / PIECES;
+      if (e >= Dh) continue;
+      f32x4 a = (f32x4)(0.0f), d = (f32x4)(0.0f);
+      float mx = kLow, sum = 0.0f;
+      const uint32_t off = (uint32_t)from * kSlotBytes + (uint32_t)(brow * LROW) * 4u;
+      for (int j0 = 0; j0 < n; j0 += NB) {
+        f32x4 ml[NB], pa[NB], pd[NB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const uint32_t at = off + (uint32_t)(min(j0 + j, n - 1) * step) * kSlotBytes;
+          ml[j] = ld_f4(wsr, at + DHP * 4u);
+          pa[j] = ld_f4(wsr, at + (uint32_t)e * 4u);
+          pd[j] = ld_f4(wsr, at + (uint32_t)e * 4u + 16u);
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          if (j0 + j >= n) break;
+          const float up = fmaxf(mx, ml[j][0]), fo = __builtin_amdgcn_exp2f(mx - up), fn = __builtin_amdgcn_exp2f(ml[j][0] - up);
+          a = a * fo + pa[j] * fn;
+          d = d * fo + pd[j] * fn;
+          sum = sum * fo + ml[j][1] * fn;
+          mx = up;
+        }
+      }
+      if (final) {
+        store_out<DT>(p, b, h, rb * ROWS + brow, e, a, d, 1.0f / sum, s_anc);
+      } else {
+        st_f4(wsr, off + (uint32_t)e * 4u, a);
+        st_f4(wsr, off + (uint32_t)e * 4u + 16u, d);
+        if (e == 0) st_f4(wsr, off + DHP * 4u, f32x4{mx, sum, 0.0f, 0.0f});
+      }
+    }
+  };
+  const int first = (k.slot - k.slot0) / kJoin * kJoin, here = min(kJoin, k.parts - first);
+  if (!last_of(here, k.slot0 + first)) return;
+  if (k.parts > kJoin) {
+    join(k.slot0 + first, 1, here, false);
+    if (!last_of((k.parts + kJoin - 1) / kJoin, k.slot0 + 1)) return;
   }
-  __syncthreads();
-  if (!s_last) return;
   if (!need_anc) {
     tree_parents(N, t < N ? p.parent[(size_t)b * N + t] : 0, p.status, s_ptr, s_anc);
     tree_ancestors(N, s_ptr, s_anc);
   }
-  constexpr int PIECES = DHP / 8, NB = 4;  // parts whose loads are in flight together
-  const int most = min(ROWS, M - rb * ROWS);
-  for (int i = t; i < most * PIECES; i += NT) {
-    const int e = i % PIECES * 8, brow = i / PIECES;
-    if (e >= Dh) continue;
-    f32x4 a = (f32x4)(0.0f), d = (f32x4)(0.0f);
-    float mx = kLow, sum = 0.0f;
-    const uint32_t off = (uint32_t)k.slot0 * kSlotBytes + (uint32_t)(brow * LROW) * 4u;
-    for (int j0 = 0; j0 < k.parts; j0 += NB) {
-      f32x4 ml[NB], pa[NB], pd[NB];
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const uint32_t at = off + (uint32_t)min(j0 + j, k.parts - 1) * kSlotBytes;
-        ml[j] = ld_f4(wsr, at + DHP * 4u);
-        pa[j] = ld_f4(wsr, at + (uint32_t)e * 4u);
-        pd[j] = ld_f4(wsr, at + (uint32_t)e * 4u + 16u);
-      }
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        if (j0 + j >= k.parts) break;
-        const float up = fmaxf(mx, ml[j][0]), fo = __builtin_amdgcn_exp2f(mx - up), fn = __builtin_amdgcn_exp2f(ml[j][0] - up);
-        a = a * fo + pa[j] * fn;
-        d = d * fo + pd[j] * fn;
-        sum = sum * fo + ml[j][1] * fn;
-        mx = up;
-      }
-    }
-    store_out<DT>(p, b, h, rb * ROWS + brow, e, a, d, 1.0f / sum, s_anc);
-  }
+  if (k.parts > kJoin) join(k.slot0, kJoin, (k.parts + kJoin - 1) / kJoin, true);
+  else join(k.slot0, 1, k.parts, true);
 }
 
 // Joins the parts of cut segments where those are of many rows: one workgroup for
@@ -1076,8 +1102,8 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
 // is quicker than a second launch.)
 template <int DT, int DHP>
 __global__ __launch_bounds__(kBlock) void k_tree_join(TreeAttnParams p, int rows) {
+  const int4 cut = p.cuts[1 + blockIdx.x];  // with the count, in one round trip
   if ((int)blockIdx.x >= p.cuts[0].x) return;
-  const int4 cut = p.cuts[1 + blockIdx.x];
   constexpr int PIECES = DHP / 8, LROW = DHP + 4, NB = 4;
   const int i = (int)(blockIdx.y * kBlock + threadIdx.x), e = i % PIECES * 8, brow = i / PIECES;
   const int h = cut.w / p.blocks, row = (cut.w - h * p.blocks) * rows + brow;
@@ -1096,6 +1122,9 @@ __global__ __launch_bounds__(kBlock) void k_tree_join(TreeAttnParams p, int rows
       pa[j] = *reinterpret_cast<const f32x4 *>(at + e);
       pd[j] = *reinterpret_cast<const f32x4 *>(at + e + 4);
     }
+    // all of them on their way before the first is waited for
+#pragma unroll
+    for (int j = 0; j < NB; ++j) asm volatile("" : "+v"(ml[j]), "+v"(pa[j]), "+v"(pd[j]));
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       if (j0 + j >= cut.y) break;

@@ -391,8 +391,8 @@ template <int DT, int DHP, int RT, int RW, int KW, bool PAGED, bool PAD>
 __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_direct_wgs(DT, DHP)) void k_tree_attention(TreeAttnParams p) {
   constexpr int NW = RW * KW, NT = NW * kWave;
   constexpr bool SHARED = RW > 1;         // keys pass through LDS, for the waves that share them
-  constexpr bool NEXT = !SHARED && RT == 1;  // registers for a second tile
   constexpr int ES = es<DT>();
+  constexpr bool NEXT = !SHARED && RT == 1 && DHP * ES <= 512;  // registers for a second tile
   constexpr int EL = 16 / ES;             // elements of a 16-byte piece
   constexpr int KS = DHP / (4 * EL);      // contraction steps of S (4 lane groups x EL elements)
   constexpr int NE = DHP / 16;            // elements of V a lane holds per key

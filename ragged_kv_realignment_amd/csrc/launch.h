@@ -42,7 +42,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeTokens = 16;          // tokens one rotary workgroup turns at most
 
 // Tree attention.
-constexpr int kMaxAttnRows = 1024;       // batch rows (their lengths' prefix sums are kept in LDS)
+constexpr int kMaxAttnRows = 1024;       // batch rows (every wave reads all their lengths, 64 at a time)
 
 // Query rows of a workgroup: rw waves of rt 16-row tiles, times kw waves that
 // take other keys; the head size is padded to dhp.
@@ -60,7 +60,7 @@ constexpr int attn_share_keys(int dtype, int dhp) { return dhp * (dtype == 0 ? 2
 // Tiles in 128 KiB of LDS (per key wave), at most eight.
 constexpr int attn_stages(int bytes) { return 131072 / bytes >= 8 ? 8 : 131072 / bytes; }
 // Workgroups per CU of four waves that share none: two of 256 registers, or one
-// of 512 where two tiles of keys take more.
+// of 512 where the keys of a tile or two take more.
 constexpr int attn_direct_wgs(int dtype, int dhp) { return dhp * (dtype == 0 ? 2 : 1) <= 128 ? 2 : 1; }
 // 16-row query tiles that a wave holds at most.
 constexpr int attn_most_tiles(int dtype, int dhp) { return dhp * (dtype == 0 ? 2 : 1) <= 128 ? 2 : 1; }
@@ -81,7 +81,7 @@ struct TreeAttnParams {
   int B, N, H, G, Dh;
   float scale;                           // its size times log2(e)
   bool negate;                           // it was negative
-  unsigned int *counters;                // workspace: a line per part, zero between calls
+  unsigned int *counters;                // workspace: a line per slot, zero between calls
   int4 *cuts;                            // the number of segments in several parts, then (first part's slot, parts, row, segment)
   void *partial;
   int partial_bytes, blocks, resident, grid;  // query blocks per head, workgroups

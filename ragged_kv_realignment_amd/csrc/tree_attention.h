@@ -7,31 +7,41 @@
 //
 // The G N query rows of one (row, KV head) share its keys, so a wave multiplies
 // them together with matrix instructions while the keys stream by once:
-//  - S^T = K Q^T: a lane holds 8 consecutive elements of one key straight from
-//    memory (16 bytes), which is the instruction's layout for K; the keys need
-//    no LDS.
+//  - S^T = K Q^T: a lane holds 8 consecutive elements of one key (16 bytes as
+//    they lie in memory), which is the instruction's layout for K.
 //  - The softmax weights come out as S^T, a lane holding one query and 8 keys of
 //    a 32-key tile; with the contraction's keys numbered in that order the same
 //    registers, rounded to the cache's type, are the operand of
 //  - O^T += V^T P^T.  For it a lane loads, for each of its 8 keys, its NE =
 //    Dh / 16 elements (a row of V is read by 16 lanes, whole), and 8 x NE
 //    elements turn into NE operands by byte permutes: element e of all 8 keys is
-//    the operand of the output rows dh = NE (lane mod 16) + e.  V needs no LDS
-//    either.
+//    the operand of the output rows dh = NE (lane mod 16) + e.
 // The running maximum is only raised when some score passes it by more than
 // 2^kSlack: below that the weights stay under 2^kSlack, exact enough in every
-// type, and the accumulators need no rescaling.  Weights and sums are fp32.
+// type, and the accumulators need no rescaling.  Weights, sums and O are fp32.
 // The weights are rounded to the cache's type for the second product (8 bits of
-// mantissa for bf16): their errors average over the keys to less than the
-// output's own rounding.
+// mantissa for bf16); their sum is taken of the rounded ones, so the roundings
+// mostly cancel in the quotient: against 64 bits the output is off by 2.2e-3 of
+// its size (bf16), of which its own rounding is 1.7e-3.
 //
-// Up to eight waves share the queries of a block (more rows per workgroup) or the
-// keys of a segment (few rows).  Waves that share keys take them through LDS.
+// Two forms (attn_shape has the rule, with both measured):
+//  - Few query rows: the waves of a workgroup take keys in turn, straight from
+//    memory to registers, a tile ahead.  Bound by memory and by latency: 79 MB of
+//    8 rows x 32 heads of 128 to 1024 positions in 22 us (3.5 TB/s; a large copy
+//    reaches 5.1), of which the split's plan takes 1.5, the first loads 1.5, and
+//    the parts' sums and joins at the end 5.
+//  - More: keys pass once through a ring of tiles in LDS for all the waves of a
+//    workgroup, by loads that write LDS directly.  Bound by instruction issue: per
+//    32-key tile and 16 query rows 17 matrix instructions beside about 110 others.
+//    16 sequences of 256 to 2048 positions, 8 heads of 96 query rows: 36 us, 82
+//    MB; 2 of 40001 and 65537, 2 heads of 1024 query rows: 144 us, 680 TFLOP/s
+//    (a large product of hipBLASLt: 1208), at which power takes the clock from 2.4
+//    to 2.0 GHz.
 //
 // A segment that is cut into parts (see plan) leaves (max, sum, O) of each in the
-// workspace.  Of up to 32 query rows, the last workgroup to arrive adds them; of
-// more, a second kernel does.  Either adds in part order, so results do not depend
-// on timing.  The order of completion in the first case uses the same scheme as
+// workspace.  In the first form the last workgroup to arrive adds them; in the
+// second another kernel does.  Either adds in part order, so results do not depend
+// on timing.  The order of completion in the first form uses the same scheme as
 // verification: sums stored past the non-coherent L2 (sc1), completed (vmcnt)
 // before the count, loaded only after the count has returned.
 #pragma once
@@ -58,12 +68,12 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 namespace {
 
-constexpr int kTile = 32;        // keys of a wave's step
-constexpr float kSlack = 8.0f;   // log2 of the largest weight before the maximum is raised
-constexpr int kWindow = 1024;       // page ids in LDS
-constexpr int kMinUnits = 4;      // of a part (see plan)
-constexpr int kJoin = 16;           // parts that one workgroup adds at once
-constexpr float kLow = -1e30f;   // running maximum before the first key
+constexpr int kTile = 32;       // keys of a wave's step
+constexpr float kSlack = 8.0f;  // log2 of the largest weight before the maximum is raised
+constexpr int kWindow = 1024;   // page ids in LDS
+constexpr int kMinUnits = 4;    // of a part (see plan)
+constexpr int kJoin = 16;       // parts that one workgroup adds at once
+constexpr float kLow = -1e30f;  // running maximum before the first key
 
 template <int DT> constexpr int es() { return DT == 0 ? 4 : 2; }
 
@@ -1096,10 +1106,11 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
 }
 
 // Joins the parts of cut segments where those are of many rows: one workgroup for
-// 256 pieces (of 8 elements) of a segment's rows, added in part order.  (The last
-// part's workgroup would take 60 us for 16 parts of 256 rows by itself, this
-// kernel under 10 with its launch; for up to 32 rows the join in the kernel above
-// is quicker than a second launch.)
+// 256 pieces (of 8 elements) of a segment's rows, added in part order.  Bound by
+// the round trips to its cut, to the parts and out: 5 us for segments of 4 parts
+// of 96 rows, 9 us for 64 parts of 256 (34 MB).  (The last part's workgroup would
+// take 60 us for 16 parts of 256 rows by itself; for up to 32 rows the join in the
+// kernel above is quicker than a second launch.)
 template <int DT, int DHP>
 __global__ __launch_bounds__(kBlock) void k_tree_join(TreeAttnParams p, int rows) {
   const int4 cut = p.cuts[1 + blockIdx.x];  // with the count, in one round trip

@@ -86,7 +86,8 @@ __device__ __forceinline__ void each_id(const float *p, int lo, int hi, const in
 // issued after the stores have completed, as in verification of a chain.
 // Bound by latency: the dependent loads (draft and parent, the gathered
 // probabilities, the stop row, the totals, the crossing run) and two barriers
-// between each.
+// between each.  8.1 us for one row of 9 nodes and 32000 ids, 10.9 us for 32 rows
+// of 24 nodes (4 MB).
 template <int VW, int NB, bool STORE_RUNS>
 __global__ __launch_bounds__(NT) void k_verify_tree_sample(TreeSampleParams p, FastDiv b_div) {
   const int B = p.B, S = p.S, R = p.R, N = p.N, V = p.V;

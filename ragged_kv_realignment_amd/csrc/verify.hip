@@ -137,7 +137,8 @@ __device__ __forceinline__ float wave_max_uniform(float v) {
 // token for each of them and parent its place.  The finish marks every node
 // whose token is its parent's choice in the parent's LDS slot (the lowest such
 // node stays), in parallel; thread 0 then follows the slots from the root, one
-// LDS round trip per accepted token.
+// LDS round trip per accepted token.  9.0 us for one row of 6 nodes and 151936
+// bf16 ids, 21 us for 16 rows of 24 (117 MB, 5.5 TB/s).
 template <int DT, bool VEC, int NT, int VPT, bool TREE>
 __global__ __launch_bounds__(NT) void k_verify_greedy(GreedyParams p, int splits, int chunk, FastDiv rows_div,
                                                       FastDiv d1_div) {

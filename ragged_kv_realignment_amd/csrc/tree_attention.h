@@ -34,7 +34,7 @@
 //    workgroup, by loads that write LDS directly.  Bound by instruction issue: per
 //    32-key tile and 16 query rows 17 matrix instructions beside about 110 others.
 //    16 sequences of 256 to 2048 positions, 8 heads of 96 query rows: 36 us, 82
-//    MB; 2 of 40001 and 65537, 2 heads of 1024 query rows: 144 us, 680 TFLOP/s
+//    MB; 2 of 40001 and 65537, 2 heads of 1024 query rows: 142 us, 686 TFLOP/s
 //    (a large product of hipBLASLt: 1208), at which power takes the clock from 2.4
 //    to 2.0 GHz.
 //
@@ -351,12 +351,12 @@ __device__ __forceinline__ bool plan(const TreeAttnParams &p, int HR, int tree_t
     if (all <= p.resident || p.resident <= segs || !__any(longest > u)) break;
     u = tries < 16 ? u + (u + 7) / 8 : 1 << 30;
   }
-  // consecutive parts on one XCD (workgroups go to the 8 XCDs in turn), so query
-  // blocks that share keys share an L2
+  // consecutive parts on one XCD (workgroups go to the 8 XCDs in turn)
   const int per_xcd = (all + 7) / 8, on_xcd = (int)(blockIdx.x >> 3);
   const int w = (int)(blockIdx.x & 7) * per_xcd + on_xcd;
   if (on_xcd >= per_xcd || w >= all) return false;
-  // all parts, in order of batch row, segment and key; those of cut segments have slots
+  // all parts, in order of batch row, head, key and query block; those of cut
+  // segments have slots, in order of segment and key
   k.cuts = 0;
   if (w == 0)
     for (int b0 = 0; b0 < p.B; b0 += kWave) k.cuts += HR * __popcll(__ballot(parts_of(rows_at(b0).units) > 1));
@@ -374,8 +374,11 @@ __device__ __forceinline__ bool plan(const TreeAttnParams &p, int HR, int tree_t
       k.start = __builtin_amdgcn_readlane(x.start, at);
       const int units = __builtin_amdgcn_readlane(x.units, at), np = __builtin_amdgcn_readlane(n, at);
       const int rel = w - before - __builtin_amdgcn_readlane(incl - mine, at);
-      k.seg = uniform((int)((uint32_t)rel / (uint32_t)np));
-      const int part = rel - k.seg * np;
+      // of a head: by part, then by query block, so that blocks that share keys
+      // run side by side on one XCD and share its L2
+      const int h = uniform((int)((uint32_t)rel / (uint32_t)(np * p.blocks))), in_head = rel - h * np * p.blocks;
+      const int part = uniform((int)((uint32_t)in_head / (uint32_t)p.blocks));
+      k.seg = h * p.blocks + in_head - part * p.blocks;
       // even parts: the first `units % np` are one longer
       const int each = uniform((int)((uint32_t)units / (uint32_t)np)), longer = units - each * np;
       k.unit0 = part * each + min(part, longer);

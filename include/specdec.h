@@ -526,6 +526,8 @@ int specdec_tree_positions(const int32_t *parent, int B, int N, const int32_t *l
  *               of row, node and head in elements (host int64[3]); a head is
  *               contiguous.  out may be x with the same strides, or must not
  *               overlap it (E_ALIAS, by the extents that the strides span).
+ *               out's dimensions nest, in any order: no stride is inside what
+ *               the shorter ones span (E_ALIAS).
  *  pos          device int32 [B][N]; a token with a negative position is left as
  *               it is in `out`.
  *  freq         device fp64 [rot/2], radians per position; the angle is formed
@@ -553,8 +555,9 @@ int specdec_rope(const void *x, const int64_t *x_strides, void *out, const int64
  *              (NULL = b; a row may be listed more than once).
  *  q, out      device, the cache's type, [B][N][q_heads][head_dim]: strides of
  *              row, node and head in elements (host int64[3]), multiples of 16
- *              bytes; a head is contiguous.  Nodes outside the tree are left as
- *              they are in `out`.
+ *              bytes; a head is contiguous, and out's dimensions nest as for
+ *              specdec_rope.  Nodes outside the tree are left as they are in
+ *              `out`.
  *  kv_new      device [layers][2][B][heads][N][head_dim].
  *  parent      the trees (above).  What nodes outside the tree hold in q and
  *              kv_new has no effect, and what a node holds only reaches itself

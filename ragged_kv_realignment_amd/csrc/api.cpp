@@ -648,6 +648,30 @@ static bool extent(const int64_t *st, int B, int N, int H, int Dh, size_t es, in
   return true;
 }
 
+// Whether no two elements of such a tensor lie at one place: its dimensions nest,
+// each one's stride past all that the shorter strides span.
+static bool distinct(const int64_t *st, int B, int N, int H, int Dh) {
+  const int n[3] = {B, N, H};
+  bool taken[3] = {n[0] == 1, n[1] == 1, n[2] == 1};
+  __int128 span = Dh;
+  for (int left = 3; left > 0; --left) {
+    int k = -1;
+    __int128 least = 0;
+    for (int j = 0; j < 3; ++j) {
+      const __int128 a = st[j] < 0 ? -(__int128)st[j] : (__int128)st[j];
+      if (!taken[j] && (k < 0 || a < least)) {
+        k = j;
+        least = a;
+      }
+    }
+    if (k < 0) break;
+    if (least < span) return false;
+    taken[k] = true;
+    span += least * (n[k] - 1);
+  }
+  return true;
+}
+
 EXPORT int specdec_rope(const void *x, const int64_t *x_strides, void *out, const int64_t *out_strides, int dtype,
                         int B, int N, int heads, int head_dim, const int32_t *pos, const double *freq, int rot,
                         int interleaved, float factor, void *stream) {
@@ -665,6 +689,7 @@ EXPORT int specdec_rope(const void *x, const int64_t *x_strides, void *out, cons
     return SPECDEC_E_ARG;
   const char *xp = static_cast<const char *>(x);
   char *op = static_cast<char *>(out);
+  if (!distinct(out_strides, B, N, heads, head_dim)) return SPECDEC_E_ALIAS;
   bool same = x == out;  // in place: the same values, each read and written by one thread
   const int n[3] = {B, N, heads};
   for (int k = 0; k < 3; ++k) same = same && (n[k] == 1 || x_strides[k] == out_strides[k]);
@@ -907,6 +932,7 @@ static int attention(sd::TreeAttnParams &p, const void *kv, size_t old_bytes, in
       !strides_ok(out_strides, B, N, q_heads, Dh, es, ol, oh, aligned))
     return SPECDEC_E_ARG;
   if (!aligned) return SPECDEC_E_ALIGN;
+  if (!distinct(out_strides, B, N, q_heads, Dh)) return SPECDEC_E_ALIAS;
   const size_t half = (size_t)B * H * N * Dh * es;
   // rows of a head (KV positions) are numbered with 32-bit integers
   if ((__int128)B * H * N >= (1LL << 31)) return SPECDEC_E_ARG;

@@ -777,7 +777,8 @@ __global__ __launch_bounds__(RW * KW * kWave, RW > 1 ? (RW * KW + 3) / 4 : attn_
     // the rows of the blocks that those lie in
     auto pages = [&](uint32_t (&at)[PASS]) {
 #pragma unroll
-      for (int j = 0; j < PASS; ++j) at[j] = PAGED ? s_page[max((pos[j] < len ? blk[j] : end_block) - window, 0)] : 0u;
+      for (int j = 0; j < PASS; ++j)  // (tiles of the tree need none, and may find no window)
+        at[j] = PAGED ? s_page[min((uint32_t)((pos[j] < len ? blk[j] : end_block) - window), kWindow - 1u)] : 0u;
     };
     // the loads of tile i, with those
     auto fetch = [&](int i, const uint32_t (&page)[PASS]) {

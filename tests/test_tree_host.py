@@ -53,6 +53,10 @@ def test_rope_host_errors():
     assert call(x=A + 1) == S.E_ALIGN
     assert call(out=A + 256) == S.E_ALIAS          # shifted by two heads
     assert call(out=A, os=_st(512, 128, 32)) == S.E_ALIAS  # the same place, other strides
+    for st in (_st(512, 0, 64), _st(0, 128, 64), _st(512, 128, 0), _st(512, 64, 64), _st(500, 128, 64), _st(512, 128, -63),
+               _st(64, 448, 64)):
+        assert call(os=st) == S.E_ALIAS            # elements of out at one place
+        assert call(x=A * 2, xs=st, os=st) == S.E_ALIAS
     assert call(B=1 << 20, N=1 << 12) == S.E_ARG
     assert call(B=0) == S.OK
 
@@ -146,6 +150,8 @@ def test_attention_host_errors(paged):
     assert call(q=A * 2 + 8) == S.E_ALIGN
     assert call(kn=A * 3 + 8) == S.E_ALIGN
     assert call(qs=_st(4 * 4 * 64 + 4, 4 * 64, 64)) == S.E_ALIGN
+    for st in (_st(4 * 4 * 64, 0, 64), _st(4 * 4 * 64, 4 * 64, 0), _st(4 * 4 * 64, 64, 64), _st(64, 4 * 64, 64)):
+        assert call(os=st) == S.E_ALIAS            # elements of out at one place
     assert call(out=A * 2 + 1024) == S.E_ALIAS
     assert call(out=A * 64 + 1024) == S.E_ALIAS
     assert call(out=A * 3 + 1024) == S.E_ALIAS

@@ -71,7 +71,7 @@ namespace {
 constexpr int kTile = 32;       // keys of a wave's step
 constexpr float kSlack = 8.0f;  // log2 of the largest weight before the maximum is raised
 constexpr int kWindow = 1024;   // page ids in LDS
-constexpr int kMinUnits = 4;    // of a part (see plan)
+constexpr int kMinUnits = 2;    // of a part (see plan)
 constexpr int kJoin = 16;       // parts that one workgroup adds at once
 constexpr float kLow = -1e30f;  // running maximum before the first key
 
@@ -298,7 +298,9 @@ struct Chunk {
 //    per segment, and grows by an eighth until the parts fit).
 //  - With more, u is a resident workgroup's share of the work: long rows are cut
 //    to it, the others stay whole, and the launch runs them as places fall free.
-//  - Parts under kMinUnits gain nothing.
+//  - Parts under kMinUnits gain nothing: one token over 300, 700, 2000 and 8000
+//    positions of 8 heads takes 8.1, 9.9, 12.0 and 17.0 us with at least 4 units,
+//    8.7, 8.9, 10.8 and 15.8 with 2, 7.9, 8.7, 12.1 and 16.6 with 1.
 // Every wave works it out by itself from the lengths, 64 rows at a time, a row per
 // lane.  Returns false where there is nothing for this workgroup.
 template <int KW>

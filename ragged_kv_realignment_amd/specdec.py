@@ -655,18 +655,30 @@ def _on(dev, *named):
 
 def _is(t, dtype, shape, at):
     """A contiguous tensor of this type and shape on GPU `at`."""
-    return t.dtype is dtype and t.shape == shape and t.get_device() == at and t.is_contiguous()
+    return t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == at and t.is_contiguous()
 
 
 def _ints(shape, dev, *named):
     """Required contiguous int32 tensors of one shape on `dev`."""
-    at = -2 if dev.index is None else dev.index
     for t, n in named:
-        if t is None or not _is(t, _I32, shape, at):
-            _need(t, n, _I32)
-            if tuple(t.shape) != tuple(shape):
-                raise ValueError("%s must have shape %s" % (n, list(shape)))
-            _on(dev, (t, n))
+        _need(t, n, _I32)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError("%s must have shape %s" % (n, list(shape)))
+    _on(dev, *named)
+
+
+# torch's allocation without its dispatcher, where this torch has it: 0.7 us an
+# output in place of 1.5 by new_empty.
+_empty_cuda = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
+_empty_cuda = getattr(_empty_cuda, "_empty_strided_cuda", None)
+
+
+def _new_ints(like, at, *shape):
+    """An uninitialised contiguous int32 tensor of one or two dimensions, on GPU
+    `at` as `like` is."""
+    if _empty_cuda is not None and at == torch._C._cuda_getDevice():
+        return _empty_cuda(shape, (1,) if len(shape) == 1 else (max(shape[1], 1), 1), _I32)
+    return like.new_empty(shape, dtype=_I32)
 
 
 def _launch(at, name, *args):
@@ -710,9 +722,9 @@ def tree_positions(parent, lens, rows=None, pos=None, status=None):
         _need(lens, "lens", _I32)
         _on(parent.device, (lens, "lens"))
         raise ValueError("lens must hold one length per row")
-    if rows is not None:
+    if rows is not None and not _is(rows, _I32, (B,), at):
         _ints((B,), parent.device, (rows, "rows"))
-    pos = parent.new_empty((B, N)) if pos is None else _out(pos, "pos", B * N, device=parent.device)
+    pos = _new_ints(parent, at, B, N) if pos is None else _out(pos, "pos", B * N, device=parent.device)
     if status is not None:
         _out(status, "status", 1, device=parent.device)
     _launch(at, "specdec_tree_positions", parent.data_ptr(), B, N, lens.data_ptr(), _ptr(rows), n, pos.data_ptr(),
@@ -776,7 +788,8 @@ def rope(x, pos, freq, interleaved=False, factor=1.0, out=None):
     xs = _heads_view(x, "x")
     B, N, H, Dh = shape = x.shape
     at = x.get_device()
-    _ints((B, N), x.device, (pos, "pos"))
+    if not _is(pos, _I32, (B, N), at):
+        _ints((B, N), x.device, (pos, "pos"))
     half = freq.numel()
     if not _is(freq, torch.float64, (half,), at):
         _need(freq, "freq", torch.float64)
@@ -788,17 +801,18 @@ def rope(x, pos, freq, interleaved=False, factor=1.0, out=None):
         raise ValueError("out must have x's shape and type")
     elif out.get_device() != at:
         raise ValueError("out must be on %s" % x.device)
-    _launch(at, "specdec_rope", x.data_ptr(), xs, out.data_ptr(), xs if out is x else _heads_view(out, "out"),
+    _launch(at, "specdec_rope", x.data_ptr(), xs, out.data_ptr(),
+            xs if out.stride() == x.stride() else _heads_view(out, "out"),
             _TORCH_DT[x.dtype], B, N, H, Dh, pos.data_ptr(), freq.data_ptr(), 2 * half, 1 if interleaved else 0, float(factor))
     return out
 
 
-def _verified(draft, B, depth, accept_len, next_token, path):
+def _verified(draft, at, B, depth, accept_len, next_token, path):
     """The outputs of a tree's verification: the caller's, or new ones."""
     dev = draft.device
-    return (draft.new_empty((B,)) if accept_len is None else _out(accept_len, "accept_len", B, device=dev),
-            draft.new_empty((B,)) if next_token is None else _out(next_token, "next_token", B, device=dev),
-            draft.new_empty((B, depth + 1)) if path is None else _out(path, "path", B * (depth + 1), device=dev))
+    return (_new_ints(draft, at, B) if accept_len is None else _out(accept_len, "accept_len", B, device=dev),
+            _new_ints(draft, at, B) if next_token is None else _out(next_token, "next_token", B, device=dev),
+            _new_ints(draft, at, B, depth + 1) if path is None else _out(path, "path", B * (depth + 1), device=dev))
 
 
 def verify_tree_greedy(logits, draft, parent, depth, ws=None, status=None, accept_len=None, next_token=None, path=None,
@@ -813,8 +827,9 @@ def verify_tree_greedy(logits, draft, parent, depth, ws=None, status=None, accep
         raise ValueError("a tree has one node at least")
     at = logits.get_device()
     depth = _depth(depth)
-    _ints((B, N), logits.device, (draft, "draft"), (parent, "parent"))
-    accept_len, next_token, path = _verified(draft, B, depth, accept_len, next_token, path)
+    if not (_is(draft, _I32, (B, N), at) and _is(parent, _I32, (B, N), at)):
+        _ints((B, N), logits.device, (draft, "draft"), (parent, "parent"))
+    accept_len, next_token, path = _verified(draft, at, B, depth, accept_len, next_token, path)
     if target_tok is not None:
         _out(target_tok, "target_tok", B * N, device=logits.device)
     if status is not None:
@@ -841,13 +856,14 @@ def verify_tree_sample(p, draft, parent, u_accept, u_draw, depth, ws=None, statu
         raise ValueError("p must be [B, N, V]")
     B, N, V = p.shape
     depth = _depth(depth)
-    _ints((B, N), p.device, (draft, "draft"), (parent, "parent"))
+    if not (_is(draft, _I32, (B, N), at) and _is(parent, _I32, (B, N), at)):
+        _ints((B, N), p.device, (draft, "draft"), (parent, "parent"))
     for t, n in ((u_accept, "u_accept"), (u_draw, "u_draw")):
         if not _is(t, torch.float32, (B, N), at):
             _need(t, n, torch.float32)
             _on(p.device, (t, n))
             raise ValueError("%s must be [B, N]" % n)
-    accept_len, next_token, path = _verified(draft, B, depth, accept_len, next_token, path)
+    accept_len, next_token, path = _verified(draft, at, B, depth, accept_len, next_token, path)
     if status is not None:
         _out(status, "status", 1, device=p.device)
     if ws is None and B > 0:
@@ -874,9 +890,10 @@ def tree_compact(kv_new, draft, path, accept_len, kv_path=None, draft_path=None,
         raise ValueError("path must be [B, depth+1]")
     depth = _depth(path.shape[1] - 1)
     dev = kv_new.device
-    _ints((B, depth + 1), dev, (path, "path"))
-    _ints((B, N), dev, (draft, "draft"))
-    _ints((B,), dev, (accept_len, "accept_len"))
+    if not (_is(path, _I32, (B, depth + 1), at) and _is(draft, _I32, (B, N), at) and _is(accept_len, _I32, (B,), at)):
+        _ints((B, depth + 1), dev, (path, "path"))
+        _ints((B, N), dev, (draft, "draft"))
+        _ints((B,), dev, (accept_len, "accept_len"))
     shape = (L, 2, B, H, depth + 1, Dh)
     if kv_path is None:
         kv_path = kv_new.new_empty(shape)
@@ -885,7 +902,7 @@ def tree_compact(kv_new, draft, path, accept_len, kv_path=None, draft_path=None,
         _on(dev, (kv_path, "kv_path"))
         raise ValueError("kv_path must be [L, 2, B, H, depth+1, Dh]")
     if draft_path is None:
-        draft_path = draft.new_empty((B, depth))
+        draft_path = _new_ints(draft, at, B, depth)
     elif not _is(draft_path, _I32, (B, depth), at):
         _out(draft_path, "draft_path", B * depth, device=dev)
     if status is not None:
@@ -936,8 +953,9 @@ def tree_attention(q, cache, layer, kv_new, parent, rows=None, group=0, scale=No
         _need(kv_new, "kv_new", dt)
         _on(q.device, (kv_new, "kv_new"))
         raise ValueError("kv_new must be [L, 2, B, H, N, Dh] of the cache's geometry")
-    _ints((B, N), q.device, (parent, "parent"))
-    if rows is not None:
+    if not _is(parent, _I32, (B, N), at):
+        _ints((B, N), q.device, (parent, "parent"))
+    if rows is not None and not _is(rows, _I32, (B,), at):
         _ints((B,), q.device, (rows, "rows"))
     if out is None:
         out = q.new_empty(shape)
@@ -954,8 +972,8 @@ def tree_attention(q, cache, layer, kv_new, parent, rows=None, group=0, scale=No
     elif ws.dtype is not torch.uint8 or ws.get_device() != at or not ws.is_contiguous():
         _out(ws, "ws", 1, torch.uint8, device=q.device)
     rest = (int(layer), q.data_ptr(), qs, Hq, kv_new.data_ptr(), parent.data_ptr(), B, N,
-            Dh ** -0.5 if scale is None else float(scale), out.data_ptr(), _heads_view(out, "out"), ws.data_ptr(), ws.numel(),
-            _ptr(status))
+            Dh ** -0.5 if scale is None else float(scale), out.data_ptr(),
+            qs if out.stride() == q.stride() else _heads_view(out, "out"), ws.data_ptr(), ws.numel(), _ptr(status))
     if paged:
         _launch(at, "specdec_tree_attention_paged", C.byref(cache.c), _ptr(rows), *rest)
     else:

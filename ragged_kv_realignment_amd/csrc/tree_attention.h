@@ -237,7 +237,9 @@ __device__ __forceinline__ void tree_ancestors(int N, int *ptr, uint32_t (*anc)[
 // Loads that write LDS directly: lane i's 16 bytes go to byte `to` (the same in all
 // lanes) of LDS + 16 i.  They have no output register; wait_loads() waits for them.
 // (The compiler, which would know the builtin's write to LDS, has every read of LDS
-// wait for all of them, the next tiles' too.)
+// wait for all of them, the next tiles' too.  It keeps nothing in M0 from one
+// instruction to another; the s_nop is the wait state that a read of M0 needs after
+// its write.)
 __device__ __forceinline__ void load_lds(const void *from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory");
 }
